@@ -32,9 +32,12 @@ FP8_ERR_NONFINITE, FP8_ERR_TIMEOUT, FP8_ERR_CUDA, FP8_ERR_WORKSPACE = 4, 5, 6, 7
 EXPORTED = ("fp8_abi_version", "fp8_status_string", "fp8_device_check", "fp8_workspace_size",
             "fp8_quantize", "fp8_scaled_gemm", "fp8_linear_forward", "fp8_linear_forward_noalloc",
             "fp8_amax", "fp8_quantize_with_amax", "fp8_scaled_gemm_ex", "fp8_linear_forward_ex",
-            "fp8_weight_only_linear", "fp8_testing_set_wait_limit_ns", "fp8_testing_encode_f32_range")
+            "fp8_weight_only_linear", "fp8_scaled_gemm_act", "fp8_linear_forward_act", "fp8_rmsnorm_quantize",
+            "fp8_testing_set_wait_limit_ns", "fp8_testing_encode_f32_range")
 FP8_WEIGHT_ONLY_MAX_TOKENS = 64
 FP8_NOALLOC_SCRATCH_BYTES = 4194304
+FP8_RMSNORM_MAX_COLS = 32768
+FP8_ACT_NONE, FP8_ACT_RELU, FP8_ACT_GELU, FP8_ACT_GELU_TANH, FP8_ACT_SILU = 0, 1, 2, 3, 4
 
 
 class fp8_history_t(ctypes.Structure):
@@ -45,6 +48,11 @@ class fp8_history_t(ctypes.Structure):
 class fp8_epilogue_t(ctypes.Structure):
     _fields_ = [("bias_dev", ctypes.c_void_p), ("amax_dev", ctypes.c_void_p), ("yq_dev", ctypes.c_void_p),
                 ("yq_scale_dev", ctypes.c_void_p), ("yq_fmt", ctypes.c_int32), ("ldq", ctypes.c_int64)]
+
+
+class fp8_epilogue_act_t(ctypes.Structure):
+    _fields_ = [("base", fp8_epilogue_t), ("activation", ctypes.c_int32), ("residual_dev", ctypes.c_void_p),
+                ("ldres", ctypes.c_int64)]
 
 
 _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
@@ -73,6 +81,16 @@ _lib.fp8_linear_forward_ex.restype = _I32
 _lib.fp8_linear_forward_ex.argtypes = [_P, _I64, _I64, _I64, _I32, _I32, ctypes.POINTER(fp8_history_t), _P, _P,
                                        _I32, _I32, _I64, _P, _I64, ctypes.POINTER(fp8_epilogue_t), _P, _P, _SZ,
                                        _P]
+_lib.fp8_scaled_gemm_act.restype = _I32
+_lib.fp8_scaled_gemm_act.argtypes = [_P, _P, _I32, _I32, _P, _P, _I32, _I32, _I64, _I64, _I64, _P, _I64,
+                                     ctypes.POINTER(fp8_epilogue_act_t), _P, _P, _SZ, _P]
+_lib.fp8_linear_forward_act.restype = _I32
+_lib.fp8_linear_forward_act.argtypes = [_P, _I64, _I64, _I64, _I32, _I32, ctypes.POINTER(fp8_history_t), _P, _P,
+                                        _I32, _I32, _I64, _P, _I64, ctypes.POINTER(fp8_epilogue_act_t), _P, _P, _SZ,
+                                        _P]
+_lib.fp8_rmsnorm_quantize.restype = _I32
+_lib.fp8_rmsnorm_quantize.argtypes = [_P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, ctypes.c_float, _I32, _I32, _P, _P,
+                                      _P, _P, _P, _P]
 _lib.fp8_weight_only_linear.restype = _I32
 _lib.fp8_weight_only_linear.argtypes = [_P, _I64, _I64, _I64, _P, _P, _I32, _I32, _I64, _P, _I64, _P, _P]
 _lib.fp8_testing_set_wait_limit_ns.restype = None
@@ -276,6 +294,84 @@ def fp8_linear_forward_ex(x, x_fmt, x_mode, w, w_scale, w_mode, w_fmt, y, worksp
     _check(rc, "fp8_linear_forward_ex")
 
 
+def _epilogue_act(M, N, bias, activation, residual, amax, yq, yq_scale, yq_fmt):
+    if residual is not None and (residual.dtype != torch.bfloat16 or tuple(residual.shape) != (M, N)
+                                 or (N > 1 and residual.stride(1) != 1)):
+        raise TypeError("residual must be bf16 [M, N] with unit column stride")
+    base = _epilogue(N, bias, amax, yq, yq_scale, yq_fmt) or fp8_epilogue_t()
+    ldres = 0 if residual is None else (residual.stride(0) if M > 1 else N)
+    return fp8_epilogue_act_t(base, activation, _ptr(residual), ldres)
+
+
+def fp8_scaled_gemm_act(a, a_scale, a_mode, fmt_a, b, b_scale, b_mode, fmt_b, y, *, bias=None,
+                        activation=FP8_ACT_NONE, residual=None, amax=None, yq=None, yq_scale=None, yq_fmt=FP8_E4M3,
+                        dev_status=None, workspace=None, stream=None):
+    """y = act(scaled a . b^T + bias) + residual, with the options of fp8_scaled_gemm_ex.  residual
+    (bf16 [M, N]) may be y itself; y may be None when yq is given."""
+    if a.dtype != torch.uint8 or b.dtype != torch.uint8 or (y is not None and y.dtype != torch.bfloat16):
+        raise TypeError("a, b must be uint8 codes and y bf16")
+    M, K = a.shape
+    N = b.shape[0]
+    ldy = 0 if y is None else (y.stride(0) if y.shape[0] > 1 else y.shape[1])
+    epi = _epilogue_act(M, N, bias, activation, residual, amax, yq, yq_scale, yq_fmt)
+    rc = _lib.fp8_scaled_gemm_act(_ptr(a), _ptr(a_scale), a_mode, fmt_a, _ptr(b), _ptr(b_scale), b_mode, fmt_b,
+                                  M, N, K, _ptr(y), ldy, ctypes.byref(epi), _ptr(dev_status), _ptr(workspace),
+                                  _nbytes(workspace), _stream(stream))
+    _check(rc, "fp8_scaled_gemm_act")
+
+
+def fp8_linear_forward_act(x, x_fmt, x_mode, w, w_scale, w_mode, w_fmt, y, workspace, *, hist: History | None = None,
+                           bias=None, activation=FP8_ACT_NONE, residual=None, amax=None, yq=None, yq_scale=None,
+                           yq_fmt=FP8_E4M3, dev_status=None, stream=None):
+    """fp8_linear_forward with the epilogue of fp8_scaled_gemm_act."""
+    if x.dtype != torch.bfloat16 or w.dtype != torch.uint8 or (y is not None and y.dtype != torch.bfloat16):
+        raise TypeError("x bf16, w uint8 codes, y bf16")
+    M, K = x.shape
+    N = w.shape[0]
+    ldx = x.stride(0) if M > 1 else K
+    ldy = 0 if y is None else (y.stride(0) if y.shape[0] > 1 else y.shape[1])
+    epi = _epilogue_act(M, N, bias, activation, residual, amax, yq, yq_scale, yq_fmt)
+    rc = _lib.fp8_linear_forward_act(_ptr(x), M, K, ldx, x_fmt, x_mode,
+                                     ctypes.byref(hist.c) if hist is not None else None, _ptr(w), _ptr(w_scale),
+                                     w_mode, w_fmt, N, _ptr(y), ldy, ctypes.byref(epi), _ptr(dev_status),
+                                     _ptr(workspace), _nbytes(workspace), _stream(stream))
+    _check(rc, "fp8_linear_forward_act")
+
+
+def _rows_of(t, name, rows, cols):
+    """Row stride of a bf16 [rows, cols] tensor with unit column stride."""
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != (rows, cols) or (t.numel() and t.stride(1) != 1):
+        raise TypeError(f"{name} must be bf16 [{rows}, {cols}] with unit column stride")
+    return t.stride(0) if rows > 1 and cols else cols
+
+
+def fp8_rmsnorm_quantize(x, weight, eps, fmt, mode, q, scale, *, residual=None, sum_out=None, y=None, amax=None,
+                         dev_status=None, stream=None):
+    """h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight; (q, scale) = y quantized (ROW, BLOCK_1x128,
+    MX32, or TENSOR with the scale of the device amax).  sum_out (may be x or residual) receives h, y the
+    normalised rows, both bf16."""
+    if x.dim() != 2:
+        raise TypeError("x must be a 2-D bf16 tensor with unit column stride")
+    rows, cols = x.shape
+    ldx = _rows_of(x, "x", rows, cols)
+    ldr = 0 if residual is None else _rows_of(residual, "residual", rows, cols)
+    lds = 0 if sum_out is None else _rows_of(sum_out, "sum_out", rows, cols)
+    if weight is not None and (weight.dtype != torch.bfloat16 or weight.numel() != cols or not weight.is_contiguous()):
+        raise TypeError("weight must be bf16 [cols]")
+    if q.dtype != torch.uint8 or tuple(q.shape) != (rows, cols) or not q.is_contiguous():
+        raise TypeError("q must be dense uint8 [rows, cols]")
+    want = torch.uint8 if mode == FP8_SCALE_MX32 else torch.float32
+    if scale.dtype != want or not scale.is_contiguous() or (mode in _SCALE_MODES and
+                                                            scale.numel() < _numel(scale_shape(mode, rows, cols))):
+        raise TypeError("scale must be a dense buffer of the mode's scales")
+    if y is not None and (y.dtype != torch.bfloat16 or tuple(y.shape) != (rows, cols) or not y.is_contiguous()):
+        raise TypeError("y must be dense bf16 [rows, cols]")
+    rc = _lib.fp8_rmsnorm_quantize(_ptr(x), rows, cols, ldx, _ptr(residual), ldr, _ptr(sum_out), lds, _ptr(weight),
+                                   float(eps), fmt, mode, _ptr(amax), _ptr(q), _ptr(scale), _ptr(y), _ptr(dev_status),
+                                   _stream(stream))
+    _check(rc, "fp8_rmsnorm_quantize")
+
+
 def fp8_weight_only_linear(x, w, w_scale, w_mode, w_fmt, y, *, dev_status=None, stream=None):
     """y [M, N] bf16 = x [M, K] bf16 times the FP8 weight w [N, K] (codes) with its scale."""
     if x.dtype != torch.bfloat16 or w.dtype != torch.uint8 or y.dtype != torch.bfloat16:
@@ -308,6 +404,17 @@ def fp8_linear_forward_noalloc(x, x_fmt, x_mode, w, w_scale, w_mode, w_fmt, y, *
 
 
 # ------------------------------------------------------------------ allocation helpers
+_SCALE_MODES = (FP8_SCALE_TENSOR, FP8_SCALE_ROW, FP8_SCALE_BLOCK_1x128, FP8_SCALE_BLOCK_128x128, FP8_SCALE_MX32,
+                FP8_SCALE_DELAYED)
+
+
+def _numel(shape) -> int:
+    n = 1
+    for d in shape:
+        n *= d
+    return n
+
+
 def scale_shape(mode: int, rows: int, cols: int):
     if mode in (FP8_SCALE_TENSOR, FP8_SCALE_DELAYED):
         return (1,)

@@ -142,6 +142,31 @@ int32_t check_epilogue(const fp8_epilogue_t* e, int64_t N) {
     return FP8_OK;
 }
 
+// The activation and residual that an entry point adds to an fp8_epilogue_t.
+struct ActOptions {
+    int32_t activation = FP8_ACT_NONE;
+    const void* residual = nullptr;
+    int64_t ldres = 0;
+    bool active() const { return activation != FP8_ACT_NONE || residual != nullptr; }
+};
+
+ActOptions act_options(const fp8_epilogue_act_t* e) {
+    ActOptions o;
+    if (e != nullptr) {
+        o.activation = e->activation;
+        o.residual = e->residual_dev;
+        o.ldres = e->ldres;
+    }
+    return o;
+}
+
+int32_t check_act(const ActOptions& o, int64_t N, const void* y, int64_t ldy) {
+    if (o.activation < FP8_ACT_NONE || o.activation > FP8_ACT_SILU) return FP8_ERR_INVALID_ARG;
+    if (o.residual == nullptr) return FP8_OK;
+    if (o.ldres < N || (o.residual == y && o.ldres != ldy)) return FP8_ERR_INVALID_ARG;
+    return (reinterpret_cast<uintptr_t>(o.residual) & 1u) != 0 ? FP8_ERR_ALIGNMENT : FP8_OK;
+}
+
 int32_t check_gemm_args(const uint8_t* a, const void* sa, int32_t am, int32_t fa, const uint8_t* b, const void* sb,
                         int32_t bm, int32_t fb, int64_t M, int64_t N, int64_t K, const void* y, int64_t ldy,
                         const fp8_epilogue_t* epi = nullptr) {
@@ -172,10 +197,11 @@ int32_t check_gemm_args(const uint8_t* a, const void* sa, int32_t am, int32_t fa
 
 int32_t gemm_impl(const uint8_t* a, const void* sa, int32_t am, int32_t fa, const uint8_t* b, const void* sb,
                   int32_t bm, int32_t fb, int64_t M, int64_t N, int64_t K, void* y, int64_t ldy, int32_t* status,
-                  cudaStream_t st, const fp8_epilogue_t* epi = nullptr, bool a_just_quantized = false) {
+                  cudaStream_t st, const fp8_epilogue_t* epi = nullptr, bool a_just_quantized = false,
+                  const ActOptions& act = {}) {
     if (M == 0 || N == 0) return FP8_OK;
     const bool ext = epi_active(epi);
-    if (K == 0 && !ext) return cuda_status(launch_zero_output(static_cast<uint16_t*>(y), M, N, ldy, st));
+    if (K == 0 && !ext && !act.active()) return cuda_status(launch_zero_output(static_cast<uint16_t*>(y), M, N, ldy, st));
     GemmArgs g{};
     if (ext) {
         g.bias = static_cast<const uint16_t*>(epi->bias_dev);
@@ -185,6 +211,9 @@ int32_t gemm_impl(const uint8_t* a, const void* sa, int32_t am, int32_t fa, cons
         g.yq_fmt = epi->yq_fmt;
         g.ldq = epi->ldq;
     }
+    g.activation = act.activation;
+    g.residual = static_cast<const uint16_t*>(act.residual);
+    g.ldres = act.ldres;
     g.a = a;
     g.b = b;
     g.sa = sa;
@@ -202,6 +231,35 @@ int32_t gemm_impl(const uint8_t* a, const void* sa, int32_t am, int32_t fa, cons
     g.a_from_previous_kernel = a_just_quantized;
     if (K == 0) return cuda_status(launch_zero_k_epilogue(g, st));
     return cuda_status(launch_gemm(g, st));
+}
+
+// fp8_linear_forward with every epilogue option: quantise X into the workspace, then the GEMM.
+int32_t linear_impl(const void* x_dev, int64_t M, int64_t K, int64_t ldx, int32_t x_fmt, int32_t x_mode,
+                    fp8_history_t* hist, const uint8_t* w_dev, const void* w_scale_dev, int32_t w_mode, int32_t w_fmt,
+                    int64_t N, void* y_dev, int64_t ldy, const fp8_epilogue_t* epi, const ActOptions& act,
+                    int32_t* dev_status, void* workspace_dev, size_t ws_bytes, void* stream) {
+    if (x_mode == FP8_SCALE_BLOCK_128x128) return FP8_ERR_INVALID_ARG;   // activations use 1x128 blocks
+    const size_t need = fp8_workspace_size(2, M, N, K, x_mode);
+    if (need == 0) return FP8_ERR_INVALID_ARG;
+    if (workspace_dev == nullptr || ws_bytes < need) return FP8_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace_dev) & 255u) != 0) return FP8_ERR_ALIGNMENT;
+    uint8_t* ws = static_cast<uint8_t*>(workspace_dev);
+    uint8_t* xq = ws;
+    void* xs = ws + align_up((size_t)(M * K), 256);
+    void* part = ws + align_up((size_t)(M * K), 256) + align_up((size_t)scale_bytes(x_mode, M, K), 256);
+    int32_t rc = check_quantize_args(x_dev, M, K, ldx, x_fmt, x_mode, xq, xs, hist, nullptr);
+    if (rc != FP8_OK) return rc;
+    const int32_t gm_a = x_mode == FP8_SCALE_DELAYED ? FP8_SCALE_TENSOR : x_mode;
+    rc = check_gemm_args(xq, xs, gm_a, x_fmt, w_dev, w_scale_dev, w_mode, w_fmt, M, N, K, y_dev, ldy, epi);
+    if (rc != FP8_OK) return rc;
+    if ((rc = check_act(act, N, y_dev, ldy)) != FP8_OK) return rc;
+    if ((rc = device_gate()) != FP8_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    rc = quantize_impl(x_dev, M, K, ldx, x_fmt, x_mode, xq, xs, hist, nullptr, dev_status, part, partials_bytes(), st);
+    if (rc != FP8_OK) return rc;
+    // the quantize kernel just enqueued wrote X's codes and scales and nothing else
+    return gemm_impl(xq, xs, gm_a, x_fmt, w_dev, w_scale_dev, w_mode, w_fmt, M, N, K, y_dev, ldy, dev_status, st, epi,
+                     /*a_just_quantized=*/true, act);
 }
 
 }  // namespace
@@ -332,6 +390,68 @@ int32_t fp8_scaled_gemm_ex(const uint8_t* a_dev, const void* a_scale_dev, int32_
                      dev_status, static_cast<cudaStream_t>(stream), epi);
 }
 
+int32_t fp8_scaled_gemm_act(const uint8_t* a_dev, const void* a_scale_dev, int32_t a_mode, int32_t fmt_a,
+                            const uint8_t* b_dev, const void* b_scale_dev, int32_t b_mode, int32_t fmt_b, int64_t M,
+                            int64_t N, int64_t K, void* y_dev, int64_t ldy, const fp8_epilogue_act_t* epi,
+                            int32_t* dev_status, void* workspace_dev, size_t ws_bytes, void* stream) {
+    (void)workspace_dev;
+    (void)ws_bytes;
+    const fp8_epilogue_t* base = epi != nullptr ? &epi->base : nullptr;
+    const ActOptions act = act_options(epi);
+    int32_t rc = check_gemm_args(a_dev, a_scale_dev, a_mode, fmt_a, b_dev, b_scale_dev, b_mode, fmt_b, M, N, K, y_dev,
+                                 ldy, base);
+    if (rc != FP8_OK) return rc;
+    if ((rc = check_act(act, N, y_dev, ldy)) != FP8_OK) return rc;
+    if ((rc = device_gate()) != FP8_OK) return rc;
+    return gemm_impl(a_dev, a_scale_dev, a_mode, fmt_a, b_dev, b_scale_dev, b_mode, fmt_b, M, N, K, y_dev, ldy,
+                     dev_status, static_cast<cudaStream_t>(stream), base, /*a_just_quantized=*/false, act);
+}
+
+int32_t fp8_rmsnorm_quantize(const void* x_dev, int64_t rows, int64_t cols, int64_t ldx, const void* residual_dev,
+                             int64_t ldr, void* sum_dev, int64_t lds, const void* weight_dev, float eps, int32_t fmt,
+                             int32_t mode, const float* amax_dev, uint8_t* q_dev, void* scale_dev, void* y_dev,
+                             int32_t* dev_status, void* stream) {
+    if (mode != FP8_SCALE_TENSOR && mode != FP8_SCALE_ROW && mode != FP8_SCALE_BLOCK_1x128 && mode != FP8_SCALE_MX32)
+        return FP8_ERR_INVALID_ARG;
+    if ((mode == FP8_SCALE_TENSOR) != (amax_dev != nullptr)) return FP8_ERR_INVALID_ARG;
+    int32_t rc = check_quantize_args(x_dev, rows, cols, ldx, fmt, mode, q_dev, scale_dev, nullptr, y_dev);
+    if (rc != FP8_OK) return rc;
+    if (cols > FP8_RMSNORM_MAX_COLS || rows >= ((int64_t)1 << 31)) return FP8_ERR_INVALID_ARG;
+    if (!(eps > 0.0f) || !(eps <= 3.402823466e38f)) return FP8_ERR_INVALID_ARG;
+    if (residual_dev != nullptr && ldr < cols) return FP8_ERR_INVALID_ARG;
+    if (sum_dev != nullptr) {
+        if (residual_dev == nullptr || lds < cols) return FP8_ERR_INVALID_ARG;
+        if ((sum_dev == x_dev && lds != ldx) || (sum_dev == residual_dev && lds != ldr)) return FP8_ERR_INVALID_ARG;
+    }
+    if (!aligned16(residual_dev) || !aligned16(sum_dev) || !aligned16(weight_dev)) return FP8_ERR_ALIGNMENT;
+    if ((residual_dev != nullptr && ldr % 8 != 0) || (sum_dev != nullptr && lds % 8 != 0)) return FP8_ERR_ALIGNMENT;
+    if ((reinterpret_cast<uintptr_t>(amax_dev) & 3u) != 0) return FP8_ERR_ALIGNMENT;
+    if ((rc = device_gate()) != FP8_OK) return rc;
+    NormArgs a{};
+    a.x = static_cast<const uint16_t*>(x_dev);
+    a.rows = rows;
+    a.cols = cols;
+    a.ldx = ldx;
+    a.res = static_cast<const uint16_t*>(residual_dev);
+    a.ldr = ldr;
+    a.sum = static_cast<uint16_t*>(sum_dev);
+    a.lds = lds;
+    a.weight = static_cast<const uint16_t*>(weight_dev);
+    a.eps = eps;
+    a.fmt = fmt;
+    a.mode = mode;
+    a.amax_in = amax_dev;
+    a.q = q_dev;
+    a.scale = scale_dev;
+    a.y = static_cast<uint16_t*>(y_dev);
+    a.status = dev_status;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (mode != FP8_SCALE_TENSOR && (rows == 0 || cols == 0))   // floor scales of the groups that exist
+        return quantize_impl(x_dev, rows, cols, ldx, fmt, mode, q_dev, scale_dev, nullptr, nullptr, dev_status, nullptr, 0,
+                             st);
+    return cuda_status(launch_rmsnorm_quantize(a, st));
+}
+
 int32_t fp8_weight_only_linear(const void* x_dev, int64_t M, int64_t K, int64_t ldx, const uint8_t* w_dev,
                                const void* w_scale_dev, int32_t w_mode, int32_t w_fmt, int64_t N, void* y_dev,
                                int64_t ldy, int32_t* dev_status, void* stream) {
@@ -373,27 +493,17 @@ int32_t fp8_linear_forward_ex(const void* x_dev, int64_t M, int64_t K, int64_t l
                            fp8_history_t* hist, const uint8_t* w_dev, const void* w_scale_dev, int32_t w_mode,
                               int32_t w_fmt, int64_t N, void* y_dev, int64_t ldy, const fp8_epilogue_t* epi,
                               int32_t* dev_status, void* workspace_dev, size_t ws_bytes, void* stream) {
-    if (x_mode == FP8_SCALE_BLOCK_128x128) return FP8_ERR_INVALID_ARG;   // activations use 1x128 blocks
-    const size_t need = fp8_workspace_size(2, M, N, K, x_mode);
-    if (need == 0) return FP8_ERR_INVALID_ARG;
-    if (workspace_dev == nullptr || ws_bytes < need) return FP8_ERR_WORKSPACE;
-    if ((reinterpret_cast<uintptr_t>(workspace_dev) & 255u) != 0) return FP8_ERR_ALIGNMENT;
-    uint8_t* ws = static_cast<uint8_t*>(workspace_dev);
-    uint8_t* xq = ws;
-    void* xs = ws + align_up((size_t)(M * K), 256);
-    void* part = ws + align_up((size_t)(M * K), 256) + align_up((size_t)scale_bytes(x_mode, M, K), 256);
-    int32_t rc = check_quantize_args(x_dev, M, K, ldx, x_fmt, x_mode, xq, xs, hist, nullptr);
-    if (rc != FP8_OK) return rc;
-    const int32_t gm_a = x_mode == FP8_SCALE_DELAYED ? FP8_SCALE_TENSOR : x_mode;
-    rc = check_gemm_args(xq, xs, gm_a, x_fmt, w_dev, w_scale_dev, w_mode, w_fmt, M, N, K, y_dev, ldy, epi);
-    if (rc != FP8_OK) return rc;
-    if ((rc = device_gate()) != FP8_OK) return rc;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    rc = quantize_impl(x_dev, M, K, ldx, x_fmt, x_mode, xq, xs, hist, nullptr, dev_status, part, partials_bytes(), st);
-    if (rc != FP8_OK) return rc;
-    // the quantize kernel just enqueued wrote X's codes and scales and nothing else
-    return gemm_impl(xq, xs, gm_a, x_fmt, w_dev, w_scale_dev, w_mode, w_fmt, M, N, K, y_dev, ldy, dev_status, st, epi,
-                     /*a_just_quantized=*/true);
+    return linear_impl(x_dev, M, K, ldx, x_fmt, x_mode, hist, w_dev, w_scale_dev, w_mode, w_fmt, N, y_dev, ldy, epi, {},
+                       dev_status, workspace_dev, ws_bytes, stream);
+}
+
+int32_t fp8_linear_forward_act(const void* x_dev, int64_t M, int64_t K, int64_t ldx, int32_t x_fmt, int32_t x_mode,
+                               fp8_history_t* hist, const uint8_t* w_dev, const void* w_scale_dev, int32_t w_mode,
+                               int32_t w_fmt, int64_t N, void* y_dev, int64_t ldy, const fp8_epilogue_act_t* epi,
+                               int32_t* dev_status, void* workspace_dev, size_t ws_bytes, void* stream) {
+    return linear_impl(x_dev, M, K, ldx, x_fmt, x_mode, hist, w_dev, w_scale_dev, w_mode, w_fmt, N, y_dev, ldy,
+                       epi != nullptr ? &epi->base : nullptr, act_options(epi), dev_status, workspace_dev, ws_bytes,
+                       stream);
 }
 
 int32_t fp8_linear_forward(const void* x_dev, int64_t M, int64_t K, int64_t ldx, int32_t x_fmt, int32_t x_mode,

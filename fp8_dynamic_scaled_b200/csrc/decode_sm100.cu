@@ -74,7 +74,7 @@ __device__ __forceinline__ void decode_chunk(const DecodeRange& r, int32_t j, in
 constexpr int D_EPI_WARPS = 8;             // two per TMEM lane quarter, each half of the tokens
 constexpr int D_THREADS = 32 * (2 + D_EPI_WARPS);
 
-template <bool EXT>
+template <int EXT>
 __global__ void __launch_bounds__(D_THREADS, 1)
 fp8_decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW64,
                   const __grid_constant__ CUtensorMap tmW16, const GemmParams p, const DecodeParams d) {
@@ -246,6 +246,12 @@ fp8_decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                         if (m >= p.M || !valid) continue;
                         float v = __uint_as_float(acc[t]) * (__ldg(p.sa + (int64_t)m * p.sa_stride) * sw);
                         if (EXT) v = __fadd_rn(v, bias);
+                        if (EXT == EPI_ACT) {
+                            float f[1] = {v};
+                            activate(p.activation, f);
+                            v = f[0];
+                            if (p.res) v = __fadd_rn(v, bf16bits_to_float(p.res[(int64_t)m * p.ldres + n]));
+                        }
                         const uint32_t yb = pack_bf16x2(v, 0.0f) & 0xFFFFu;
                         if (!EXT || p.write_y) p.y[(int64_t)m * p.ldy + n] = (uint16_t)yb;
                         if (EXT) {
@@ -279,7 +285,7 @@ fp8_decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     if (warp == 1) ptx::tmem_dealloc(tmem_base, 256);
 }
 
-template <bool EXT>
+template <int EXT>
 static cudaError_t launch_decode_t(const GemmArgs& g, GemmParams p, cudaStream_t st) {
     DecodeParams d{};
     d.nt = (int32_t)((g.M + 15) / 16 * 16);
@@ -331,7 +337,9 @@ static cudaError_t launch_decode_t(const GemmArgs& g, GemmParams p, cudaStream_t
 // M <= D_MAX_TOKENS, per-tensor / per-row scales (p holds the scales, epilogue
 // options, output and K-block count).
 cudaError_t launch_decode(const GemmArgs& g, const GemmParams& p, cudaStream_t st) {
-    return p.ext ? launch_decode_t<true>(g, p, st) : launch_decode_t<false>(g, p, st);
+    return p.ext == EPI_ACT ? launch_decode_t<EPI_ACT>(g, p, st)
+           : p.ext          ? launch_decode_t<EPI_OPTIONS>(g, p, st)
+                            : launch_decode_t<EPI_PLAIN>(g, p, st);
 }
 
 }  // namespace fp8b

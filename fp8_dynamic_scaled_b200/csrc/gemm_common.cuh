@@ -25,6 +25,11 @@ constexpr uint64_t WAIT_TIMEOUT_NS = 4000000000ull;   // 4 s: default limit of a
 constexpr uint64_t DRAIN_LIMIT_NS = 2000000000ull;    // 2 s: limit of a wait for hardware completion
 
 
+// What a kernel instance's epilogue can do: plain bf16 output; bias / output amax / FP8
+// output; those and an activation and a residual.  Each is its own instance, so that
+// the options cost nothing where they are not asked for.
+enum { EPI_PLAIN = 0, EPI_OPTIONS = 1, EPI_ACT = 2 };
+
 struct GemmParams {
     int32_t M, N, K;
     int32_t num_m, num_n, num_kb;
@@ -46,7 +51,7 @@ struct GemmParams {
     int32_t y_direct;
     int32_t y_vec;          // y rows start 16-byte aligned (ldy % 8 == 0, aligned base)
     int32_t sb_vec;         // per-row b scales start 16-byte aligned
-    // optional epilogue (fp8_epilogue_t); ext != 0 when any option is set
+    // optional epilogue (fp8_epilogue_t); ext (EPI_*) != 0 when any option is set
     int32_t ext;
     int32_t write_y;        // 0: no bf16 Y (FP8 output only)
     const uint16_t* bias;   // bf16 [N], 16-byte aligned, or null
@@ -56,6 +61,11 @@ struct GemmParams {
     int64_t ldq;
     int32_t yq_fmt;
     int32_t yq_vec;         // yq rows start 16-byte aligned
+    // activation and residual (fp8_epilogue_act_t; ext == EPI_ACT)
+    int32_t activation;
+    const uint16_t* res;    // bf16 [M, ldres], or null; may be y itself
+    int64_t ldres;
+    int32_t res_vec;        // residual rows start 16-byte aligned
     // launched as the programmatic dependent of the kernel that produced A (and only A);
     // every kernel waits (pdl_wait) before it reads A or the scales
     int32_t pdl;
@@ -207,10 +217,76 @@ __device__ __forceinline__ EpiState epi_init(const GemmParams& p) {
     return e;
 }
 
+// The activation on one fp32 value (fp8_activation_t).  exp and erfc in fp32: the result is
+// rounded to bf16 (2^-9) right after, far above their few ulp.  The forms keep their
+// relative accuracy in the negative tail: GELU through erfc, not 1 + erf, and its tanh
+// form as v * sigmoid(2u), not 1 + tanh(u).
+// v / (1 + exp(-z)), with the exponential of -|z|: the divisor stays in [1, 2], and a result
+// near the end of the fp32 range keeps its value.
+__device__ __forceinline__ float sigmoid_times(float v, float z) {
+    const float e = __expf(-fabsf(z));
+    return __fdividef(z >= 0.0f ? v : v * e, 1.0f + e);
+}
+template <int ACT>
+__device__ __forceinline__ float act1(float v) {
+    if (ACT == FP8_ACT_RELU) return v > 0.0f ? v : (v != v ? v : 0.0f);
+    if (ACT == FP8_ACT_GELU) return 0.5f * v * erfcf(v * -0.70710678f);
+    if (ACT == FP8_ACT_GELU_TANH) {
+        // u = sqrt(2/pi) (v + 0.044715 v^3); |v| > 16 is at its limit (0 or v) either way,
+        // and the clamp keeps v^3 finite
+        const float c = fminf(fmaxf(v, -16.0f), 16.0f);
+        return sigmoid_times(v, 1.5957691f * fmaf(0.044715f * c * c, c, c));
+    }
+    if (ACT == FP8_ACT_SILU) return sigmoid_times(v, v);
+    return v;
+}
+template <int ACT, int N>
+__device__ __forceinline__ void act_n(float (&f)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[j] = act1<ACT>(f[j]);
+}
+template <int N>
+__device__ __forceinline__ void activate(int32_t act, float (&f)[N]) {
+    switch (act) {
+    case FP8_ACT_RELU: act_n<FP8_ACT_RELU>(f); break;
+    case FP8_ACT_GELU: act_n<FP8_ACT_GELU>(f); break;
+    case FP8_ACT_GELU_TANH: act_n<FP8_ACT_GELU_TANH>(f); break;
+    case FP8_ACT_SILU: act_n<FP8_ACT_SILU>(f); break;
+    default: break;
+    }
+}
+
+// Adds 32 residual columns [n0, n0 + 32) of one row.  Plain (coherent) loads: the residual
+// may be Y itself, whose elements this lane reads here before it writes them.
+__device__ __forceinline__ void add_residual(const GemmParams& p, float (&f)[32], int32_t n0, int32_t n_lim,
+                                             int32_t row) {
+    const uint16_t* src = p.res + (int64_t)row * p.ldres + n0;
+    if (p.res_vec && n0 + 32 <= n_lim) {
+        uint4 v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = ld_v4(src + 8 * q);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t b[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[8 * q + 2 * i] = __fadd_rn(f[8 * q + 2 * i], bf16_lo(b[i]));
+                f[8 * q + 2 * i + 1] = __fadd_rn(f[8 * q + 2 * i + 1], bf16_hi(b[i]));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (n0 + j < n_lim) f[j] = __fadd_rn(f[j], bf16bits_to_float(src[j]));
+    }
+}
+
 // The options on 32 columns [n0, n0 + 32) of one output row held by this lane (only
 // columns below n_lim exist):
-// f[] are the scaled fp32 accumulators.  Adds the bias, rounds to bf16 (w, for the
-// Y store), folds |y| into the running maximum and writes the FP8 output codes.
+// f[] are the scaled fp32 accumulators.  Adds the bias, applies the activation and adds the
+// residual (EPI_ACT), rounds to bf16 (w, for the Y store), folds |y| into the running
+// maximum and writes the FP8 output codes.
+template <int EXT>
 __device__ __forceinline__ void epi_chunk(const GemmParams& p, EpiState& es, float (&f)[32], int32_t n0,
                                           int32_t n_lim, int32_t row, uint32_t (&w)[16]) {
     if (p.bias) {
@@ -235,6 +311,10 @@ __device__ __forceinline__ void epi_chunk(const GemmParams& p, EpiState& es, flo
                 f[j] = __fadd_rn(f[j], b);
             }
         }
+    }
+    if (EXT == EPI_ACT) {
+        activate(p.activation, f);
+        if (p.res && row < p.M && n0 < n_lim) add_residual(p, f, n0, n_lim, row);
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
@@ -279,7 +359,7 @@ __device__ __forceinline__ void epi_flush(const GemmParams& p, const EpiState& e
 
 // Per-tensor / per-row scales on 32 accumulator columns of one row:
 // y = acc * (s_a[m] * s_b[n]), then the plain bf16 rounding or the options.
-template <bool EXT>
+template <int EXT>
 __device__ __forceinline__ void rowscale_chunk(const GemmParams& p, EpiState& es, const uint32_t (&r)[32], float sx,
                                                int32_t n0, int32_t n_lim, int32_t row, uint32_t (&w)[16]) {
     if constexpr (!EXT) {
@@ -334,7 +414,7 @@ __device__ __forceinline__ void rowscale_chunk(const GemmParams& p, EpiState& es
                 f[j] = n < n_lim ? __uint_as_float(r[j]) * (sx * __ldg(p.sb + (int64_t)n * p.sb_stride)) : 0.0f;
             }
         }
-        epi_chunk(p, es, f, n0, n_lim, row, w);
+        epi_chunk<EXT>(p, es, f, n0, n_lim, row, w);
     }
 }
 

@@ -73,7 +73,7 @@ struct Smem {
 };
 
 // ================================================================ the kernel
-template <int V, bool EXT>
+template <int V, int EXT>
 __global__ void __launch_bounds__(Smem<V>::NT, 1)
 fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmY, const GemmParams p) {
@@ -429,7 +429,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                             f[2 * j] = acc[c * 16 + j].x;
                             f[2 * j + 1] = acc[c * 16 + j].y;
                         }
-                        epi_chunk(p, es, f, n0, p.N, row, w);
+                        epi_chunk<EXT>(p, es, f, n0, p.N, row, w);
                     }
                     if (n0 < p.N && (!EXT || p.write_y)) {
                         uint8_t* b = ybuf + (store_it % C::STAGE_BUFS) * 2048;
@@ -463,7 +463,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         float f[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(r[c][j]);
-                        epi_chunk(p, es, f, n0, p.N, row, w);
+                        epi_chunk<EXT>(p, es, f, n0, p.N, row, w);
                     }
                     if (n0 < p.N && (!EXT || p.write_y)) {
                         uint8_t* b = ybuf + (store_it % C::STAGE_BUFS) * 2048;
@@ -517,7 +517,7 @@ struct PairSmem {
     static constexpr uint32_t ALLOC = TOTAL + 1024;
 };
 
-template <bool EXT>
+template <int EXT>
 __global__ void __launch_bounds__(PairSmem::NT, 1)
 fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmY, const GemmParams p) {
@@ -707,7 +707,7 @@ uint64_t wait_limit_ns() {
     return v != 0 ? v : WAIT_TIMEOUT_NS;
 }
 
-template <int V, bool EXT>
+template <int V, int EXT>
 static cudaError_t launch_variant(const GemmArgs& g, const GemmParams& p, cudaStream_t st) {
     CUtensorMap ta, tb, ty;
     // M, N, K sizes beyond 2^31 are rejected by the API before this point.
@@ -746,7 +746,7 @@ static cudaError_t launch_variant(const GemmArgs& g, const GemmParams& p, cudaSt
 }
 
 // CTA-pair launch: clusters of two CTAs, 256 x 256 tiles.
-template <bool EXT>
+template <int EXT>
 static cudaError_t launch_pair(const GemmArgs& g, GemmParams p, cudaStream_t st) {
     p.num_m = (int32_t)((g.M + P_BM - 1) / P_BM);
     p.m_fastest = (g.M <= g.N) ? 1 : 0;
@@ -830,9 +830,21 @@ static void set_epilogue(const GemmArgs& g, GemmParams& p) {
     p.yq_fmt = g.yq_fmt;
     p.ldq = g.ldq;
     p.yq_vec = (g.yq != nullptr && (reinterpret_cast<uintptr_t>(g.yq) & 15u) == 0 && g.ldq % 16 == 0) ? 1 : 0;
-    p.ext = (g.bias != nullptr || g.amax != nullptr || g.yq != nullptr) ? 1 : 0;
+    p.ext = (g.bias != nullptr || g.amax != nullptr || g.yq != nullptr) ? EPI_OPTIONS : EPI_PLAIN;
+    if (g.activation != FP8_ACT_NONE || g.residual != nullptr) p.ext = EPI_ACT;
+    p.activation = g.activation;
+    p.res = g.residual;
+    p.ldres = g.ldres;
+    p.res_vec = (g.ldres % 8 == 0 && (reinterpret_cast<uintptr_t>(g.residual) & 15u) == 0) ? 1 : 0;
     p.write_y = g.y != nullptr ? 1 : 0;
     if (!p.write_y) p.y_direct = 1;
+}
+
+template <int V>
+static cudaError_t launch_variant_ext(const GemmArgs& g, const GemmParams& p, cudaStream_t st) {
+    return p.ext == EPI_ACT ? launch_variant<V, EPI_ACT>(g, p, st)
+           : p.ext          ? launch_variant<V, EPI_OPTIONS>(g, p, st)
+                            : launch_variant<V, EPI_PLAIN>(g, p, st);
 }
 
 cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t st) {
@@ -867,20 +879,23 @@ cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t st) {
         // a few tokens: stream W across all SMs; CTA pairs once M spans a 256-row tile;
         // a single CTA per tile in between
         if (g.M <= D_MAX_TOKENS) return launch_decode(g, p, st);
-        if (g.M >= P_BM) return p.ext ? launch_pair<true>(g, p, st) : launch_pair<false>(g, p, st);
-        return p.ext ? launch_variant<V_ROWSCALE, true>(g, p, st) : launch_variant<V_ROWSCALE, false>(g, p, st);
+        if (g.M >= P_BM)
+            return p.ext == EPI_ACT ? launch_pair<EPI_ACT>(g, p, st)
+                   : p.ext          ? launch_pair<EPI_OPTIONS>(g, p, st)
+                                    : launch_pair<EPI_PLAIN>(g, p, st);
+        return launch_variant_ext<V_ROWSCALE>(g, p, st);
     }
     if (g.a_mode == FP8_SCALE_BLOCK_1x128 && g.b_mode == FP8_SCALE_BLOCK_128x128) {
         p.sa = static_cast<const float*>(g.sa);
         p.sb = static_cast<const float*>(g.sb);
         p.idesc = idesc_f8f6f4(g.fmt_a, g.fmt_b);
-        return p.ext ? launch_variant<V_BLOCK, true>(g, p, st) : launch_variant<V_BLOCK, false>(g, p, st);
+        return launch_variant_ext<V_BLOCK>(g, p, st);
     }
     if (g.a_mode == FP8_SCALE_MX32 && g.b_mode == FP8_SCALE_MX32) {
         p.sfa = static_cast<const uint8_t*>(g.sa);
         p.sfb = static_cast<const uint8_t*>(g.sb);
         p.idesc = idesc_mx(g.fmt_a, g.fmt_b);
-        return p.ext ? launch_variant<V_MX, true>(g, p, st) : launch_variant<V_MX, false>(g, p, st);
+        return launch_variant_ext<V_MX>(g, p, st);
     }
     return cudaErrorInvalidValue;
 }
@@ -891,8 +906,10 @@ __global__ void zero_rows_kernel(uint16_t* y, int64_t M, int64_t N, int64_t ldy)
             y[r * ldy + c] = 0;
 }
 
-// K == 0 with epilogue options: every accumulator is 0, so y = bf16(0 + bias[n]).
-// One thread per (row, 32-column chunk), the same per-lane epilogue as the GEMM.
+// K == 0 with epilogue options: every accumulator is 0, so y = bf16(0 + bias[n]) (and the
+// activation and the residual).  One thread per (row, 32-column chunk), the same per-lane
+// epilogue as the GEMM.
+template <int EXT>
 __global__ void __launch_bounds__(256) epi_zero_k_kernel(const GemmParams p) {
     EpiState es = epi_init(p);
     const int lane = threadIdx.x & 31;
@@ -907,7 +924,7 @@ __global__ void __launch_bounds__(256) epi_zero_k_kernel(const GemmParams p) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) f[j] = 0.0f;
         uint32_t w[16];
-        epi_chunk(p, es, f, n0, p.N, row, w);
+        epi_chunk<EXT>(p, es, f, n0, p.N, row, w);
         if (p.write_y && row < p.M) {
             uint16_t* dst = p.y + (int64_t)row * p.ldy;
 #pragma unroll
@@ -933,7 +950,8 @@ cudaError_t launch_zero_k_epilogue(const GemmArgs& g, cudaStream_t st) {
     set_epilogue(g, p);
     const int64_t total = g.M * ((g.N + 31) / 32);
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((total + 255) / 256, (int64_t)num_sms() * 8));
-    epi_zero_k_kernel<<<grid, 256, 0, st>>>(p);
+    if (p.ext == EPI_ACT) epi_zero_k_kernel<EPI_ACT><<<grid, 256, 0, st>>>(p);
+    else                  epi_zero_k_kernel<EPI_OPTIONS><<<grid, 256, 0, st>>>(p);
     return cudaGetLastError();
 }
 

@@ -60,6 +60,9 @@ struct GemmArgs {
     const float* yq_scale;   // s_y
     int32_t yq_fmt;
     int64_t ldq;
+    int32_t activation;      // fp8_activation_t, applied after the bias
+    const uint16_t* residual;   // bf16 [M, ldres] added after the activation, or null
+    int64_t ldres;
     // the kernel just before the GEMM on the stream wrote A and its scales and nothing
     // else: the GEMM may start on B before A is ready (programmatic dependent launch)
     bool a_from_previous_kernel;
@@ -93,5 +96,24 @@ struct WoArgs {              // weight-only FP8 linear (wo_sm100.cu)
 cudaError_t launch_weight_only(const WoArgs& g, cudaStream_t st);
 cudaError_t launch_zero_output(uint16_t* y, int64_t M, int64_t N, int64_t ldy, cudaStream_t st);
 cudaError_t launch_zero_k_epilogue(const GemmArgs& g, cudaStream_t st);
+
+
+struct NormArgs {            // residual + RMSNorm + FP8 output (norm.cu)
+    const uint16_t* x;       // bf16 [rows, cols], row stride ldx
+    int64_t rows, cols, ldx;
+    const uint16_t* res;     // nullable, row stride ldr
+    int64_t ldr;
+    uint16_t* sum;           // nullable, row stride lds
+    int64_t lds;
+    const uint16_t* weight;  // nullable bf16 [cols]
+    float eps;
+    int32_t fmt, mode;
+    const float* amax_in;    // TENSOR
+    uint8_t* q;
+    void* scale;
+    uint16_t* y;             // nullable bf16 [rows, cols]
+    int32_t* status;
+};
+cudaError_t launch_rmsnorm_quantize(const NormArgs& a, cudaStream_t st);
 
 }  // namespace fp8b

@@ -1,0 +1,306 @@
+// norm.cu -- residual addition + root-mean-square norm + FP8 output (sm_100a).
+//
+//   h = x + r,  y = h / sqrt(mean(h^2) + eps) * w,  (q, s) = quantise(y)
+//
+// All in fp32 from the bf16 inputs; h, y and the codes are each rounded once from the fp32
+// values.  The work is 2 B read (4 with a residual) and 1 B written (3 with h) per element
+// and some ten instructions, so HBM bounds it: a row is read once, with every load of a
+// thread issued before the first use, stays in registers through its two reductions (the
+// sum of squares; the amax, over the row or a 128- or 32-element group of it), and is
+// written once.  The division by the scale is the corrected reciprocal of quantize.cu.
+#include "common.cuh"
+#include "kernels.h"
+
+namespace fp8b {
+
+namespace {
+
+constexpr int NVEC = 8;            // bf16 elements per 16-byte vector
+constexpr int WARP_ROWS = 8;       // rows (warps) of a CTA in the warp-per-row kernel
+
+struct NormParams {
+    const uint16_t* x;
+    const uint16_t* res;
+    uint16_t* sum;
+    const uint16_t* weight;
+    uint8_t* q;
+    void* scale;
+    uint16_t* y;
+    const float* amax_in;
+    int32_t* status;
+    int64_t rows, ldx, ldr, lds;
+    int32_t cols, nvec, nscale;    // nscale: scales per row
+    float eps, inv_cols;
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Sum (max) over the group of threads that owns a row: a warp, or the CTA through `red`.
+template <bool WARP>
+__device__ __forceinline__ float group_sum(float v, float* red) {
+    v = warp_sum(v);
+    if (WARP) return v;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    return warp_sum(lane < nw ? red[lane] : 0.0f);
+}
+template <bool WARP>
+__device__ __forceinline__ uint32_t group_max(uint32_t v, uint32_t* red) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    if (WARP) return v;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    return __reduce_max_sync(0xffffffffu, lane < nw ? red[lane] : 0u);
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
+    f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x);
+    f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
+    f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z);
+    f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
+}
+__device__ __forceinline__ uint4 pack8(const float* f) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
+// 8 fp32 values -> 8 codes of y / s (r = RN(1/s), one Markstein step, as in quantize.cu; a
+// quotient that overflows, possible with a given amax only, saturates uncorrected).
+template <int FMT, bool GUARD>
+__device__ __forceinline__ uint2 encode8(const float* y, float s, float r) {
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 ny = make_float2(-y[2 * i], -y[2 * i + 1]), nr = make_float2(-r, -r);
+        const float2 q = mul2_rn(ny, nr);
+        float2 t = fma2_rn(fma2_rn(q, make_float2(s, s), ny), nr, q);
+        if (GUARD) {
+            if (!(fabsf(q.x) <= 3.402823466e38f)) t.x = q.x;
+            if (!(fabsf(q.y) <= 3.402823466e38f)) t.y = q.y;
+        }
+        c[i] = cvt_pair<FMT>(t.x, t.y);
+    }
+    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// MODE: fp8_scaling_t.  VPT: 16-byte vectors of a row per thread.  WARP: a warp per row
+// (rows of up to 32 VPT vectors), else the CTA (blockDim.x >= nvec / VPT).
+template <int FMT, int MODE, int VPT, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * WARP_ROWS : 1024) rmsnorm_quantize_kernel(const NormParams p) {
+    __shared__ float red_sum[2][32];
+    __shared__ uint32_t red_max[32];
+    const int64_t row = WARP ? (int64_t)blockIdx.x * WARP_ROWS + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+    if (WARP && row >= p.rows) return;
+    const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
+    const int step = WARP ? 32 : blockDim.x;
+    float h[VPT][NVEC];
+    {
+        uint4 xv[VPT], rv[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int k = t + j * step;
+            xv[j] = make_uint4(0, 0, 0, 0);
+            if (k < p.nvec) xv[j] = ld_v4_stream(p.x + row * p.ldx + k * NVEC);
+        }
+        if (p.res) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int k = t + j * step;
+                rv[j] = make_uint4(0, 0, 0, 0);
+                if (k < p.nvec) rv[j] = ld_v4_stream(p.res + row * p.ldr + k * NVEC);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            unpack8(xv[j], h[j]);
+            if (p.res) {
+                float r[NVEC];
+                unpack8(rv[j], r);
+#pragma unroll
+                for (int i = 0; i < NVEC; ++i) h[j][i] = __fadd_rn(h[j][i], r[i]);
+            }
+        }
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int i = 0; i < NVEC; ++i) ss = fmaf(h[j][i], h[j][i], ss);
+    ss = group_sum<WARP>(ss, red_sum[0]);
+    if (p.sum) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int k = t + j * step;
+            if (k < p.nvec) st_v4_stream(p.sum + row * p.lds + k * NVEC, pack8(h[j]));
+        }
+    }
+    // 1 / sqrt(mean + eps); squares that leave the fp32 range (|h| above 1e19) are summed
+    // again at 2^-80 of their size.  The branch is the same for the whole row.
+    float rstd, pre = 1.0f;
+    if (ss <= 3.402823466e38f) {
+        rstd = __frsqrt_rn(fmaf(ss, p.inv_cols, p.eps));
+    } else {
+        pre = 8.271806125530277e-25f;                 // 2^-80
+        float s2 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int i = 0; i < NVEC; ++i) s2 = fmaf(h[j][i] * pre, h[j][i] * pre, s2);
+        rstd = __frsqrt_rn(group_sum<WARP>(s2, red_sum[1]) * p.inv_cols);   // eps is far below
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int k = t + j * step;
+        float w[NVEC];
+        uint4 wv = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+        if (p.weight && k < p.nvec) wv = __ldg(reinterpret_cast<const uint4*>(p.weight + k * NVEC));
+        unpack8(wv, w);
+#pragma unroll
+        for (int i = 0; i < NVEC; ++i) h[j][i] = h[j][i] * pre * rstd * w[i];
+    }
+    // from here h holds y
+    uint32_t m[VPT];
+    uint32_t all = 0;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        m[j] = 0;
+#pragma unroll
+        for (int i = 0; i < NVEC; ++i) m[j] = max(m[j], __float_as_uint(h[j][i]) & 0x7FFFFFFFu);
+        all = max(all, m[j]);
+    }
+    float s = 1.0f, r = 1.0f;
+    if (MODE == FP8_SCALE_ROW) {
+        uint32_t a = group_max<WARP>(all, red_max);
+        if (a >= 0x7F800000u) {
+            if (t == 0) report_status(p.status, FP8_ERR_NONFINITE);
+            a = 0x7F7FFFFFu;
+        }
+        s = scale_from_amax<FMT>(__uint_as_float(a));
+        r = __frcp_rn(s);
+        if (t == 0) static_cast<float*>(p.scale)[row] = s;
+    } else if (MODE == FP8_SCALE_TENSOR) {
+        if (all >= 0x7F800000u) report_status(p.status, FP8_ERR_NONFINITE);
+        float a = *p.amax_in;
+        if (!(a <= 3.402823466e38f)) {
+            if (row == 0 && t == 0) report_status(p.status, FP8_ERR_NONFINITE);
+            a = 3.402823466e38f;
+        }
+        s = scale_from_amax<FMT>(a);
+        r = __frcp_rn(s);
+        if (row == 0 && t == 0) static_cast<float*>(p.scale)[0] = s;
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int k = t + j * step;
+        if (MODE == FP8_SCALE_BLOCK_1x128 || MODE == FP8_SCALE_MX32) {
+            // a block is 16 (4) vectors, held by as many neighbouring lanes
+            uint32_t a = m[j];
+#pragma unroll
+            for (int o = MODE == FP8_SCALE_MX32 ? 2 : 8; o > 0; o >>= 1)
+                a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+            if (a >= 0x7F800000u) {
+                if (k < p.nvec) report_status(p.status, FP8_ERR_NONFINITE);
+                a = 0x7F7FFFFFu;
+            }
+            if (MODE == FP8_SCALE_MX32) {
+                const int e = mx_exponent(a >> 16);      // the exponent is in the upper bits
+                r = exp2i(-e);
+                if ((k & 3) == 0 && k < p.nvec)
+                    static_cast<uint8_t*>(p.scale)[row * p.nscale + (k >> 2)] = (uint8_t)(e + 127);
+            } else {
+                s = scale_from_amax<FMT>(__uint_as_float(a));
+                r = __frcp_rn(s);
+                if ((k & 15) == 0 && k < p.nvec) static_cast<float*>(p.scale)[row * p.nscale + (k >> 4)] = s;
+            }
+        }
+        if (k >= p.nvec) continue;
+        uint2 c;
+        if (MODE == FP8_SCALE_MX32) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = cvt_pair<FMT>(__fmul_rn(h[j][2 * i], r), __fmul_rn(h[j][2 * i + 1], r));
+            c = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+        } else {
+            c = encode8<FMT, MODE == FP8_SCALE_TENSOR>(h[j], s, r);
+        }
+        *reinterpret_cast<uint2*>(p.q + row * p.cols + k * NVEC) = c;
+        if (p.y) st_v4_stream(p.y + row * p.cols + k * NVEC, pack8(h[j]));
+    }
+}
+
+template <int FMT, int MODE, int VPT, bool WARP>
+cudaError_t launch_one(const NormParams& p, cudaStream_t st) {
+    const int64_t grid = WARP ? (p.rows + WARP_ROWS - 1) / WARP_ROWS : p.rows;
+    const int per = (p.nvec + VPT - 1) / VPT;
+    const int threads = WARP ? 32 * WARP_ROWS : std::max(32, (per + 31) / 32 * 32);
+    rmsnorm_quantize_kernel<FMT, MODE, VPT, WARP><<<(unsigned)grid, threads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <int FMT, int MODE>
+cudaError_t launch_mode(const NormParams& p, cudaStream_t st) {
+    if (p.nvec <= 32) return launch_one<FMT, MODE, 1, true>(p, st);
+    if (p.nvec <= 64) return launch_one<FMT, MODE, 2, true>(p, st);
+    if (p.nvec <= 128) return launch_one<FMT, MODE, 4, true>(p, st);
+    return launch_one<FMT, MODE, 4, false>(p, st);     // nvec <= 4096: at most 1024 threads
+}
+
+template <int FMT>
+cudaError_t launch_fmt(const NormParams& p, int32_t mode, cudaStream_t st) {
+    switch (mode) {
+    case FP8_SCALE_TENSOR: return launch_mode<FMT, FP8_SCALE_TENSOR>(p, st);
+    case FP8_SCALE_ROW: return launch_mode<FMT, FP8_SCALE_ROW>(p, st);
+    case FP8_SCALE_BLOCK_1x128: return launch_mode<FMT, FP8_SCALE_BLOCK_1x128>(p, st);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+// TENSOR with nothing to quantise still writes its scale.
+template <int FMT>
+__global__ void given_scale_kernel(const float* amax, float* scale, int32_t* status) {
+    float a = *amax;
+    if (!(a <= 3.402823466e38f)) {
+        report_status(status, FP8_ERR_NONFINITE);
+        a = 3.402823466e38f;
+    }
+    *scale = scale_from_amax<FMT>(a);
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm_quantize(const NormArgs& a, cudaStream_t st) {
+    if (a.rows == 0 || a.cols == 0) {                    // TENSOR only: the caller fills the others
+        if (a.fmt == FP8_E4M3) given_scale_kernel<FP8_E4M3><<<1, 1, 0, st>>>(a.amax_in, static_cast<float*>(a.scale), a.status);
+        else                   given_scale_kernel<FP8_E5M2><<<1, 1, 0, st>>>(a.amax_in, static_cast<float*>(a.scale), a.status);
+        return cudaGetLastError();
+    }
+    NormParams p{};
+    p.x = a.x;
+    p.res = a.res;
+    p.sum = a.sum;
+    p.weight = a.weight;
+    p.q = a.q;
+    p.scale = a.scale;
+    p.y = a.y;
+    p.amax_in = a.amax_in;
+    p.status = a.status;
+    p.rows = a.rows;
+    p.ldx = a.ldx;
+    p.ldr = a.ldr;
+    p.lds = a.lds;
+    p.cols = (int32_t)a.cols;
+    p.nvec = (int32_t)(a.cols / NVEC);
+    p.nscale = a.mode == FP8_SCALE_MX32 ? p.cols / 32 : (p.cols + 127) / 128;
+    p.eps = a.eps;
+    p.inv_cols = 1.0f / (float)a.cols;
+    if (a.mode == FP8_SCALE_MX32) return launch_mode<FP8_E4M3, FP8_SCALE_MX32>(p, st);
+    return a.fmt == FP8_E4M3 ? launch_fmt<FP8_E4M3>(p, a.mode, st) : launch_fmt<FP8_E5M2>(p, a.mode, st);
+}
+
+}  // namespace fp8b

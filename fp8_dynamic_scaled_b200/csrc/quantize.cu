@@ -68,28 +68,6 @@ __device__ __forceinline__ uint4 dequant_vec(const uint2& c, float mul) {
                       pack_bf16x2(__fmul_rn(e.x, mul), __fmul_rn(e.y, mul)));
 }
 
-// MX shared exponent from an amax bf16 pattern: floor(log2 a) is the unbiased
-// exponent of a (bf16 subnormals: position of the leading mantissa bit).
-__device__ __forceinline__ int mx_exponent(uint32_t amax_bits) {
-    if (amax_bits == 0) return -127;
-    int ebits = (int)(amax_bits >> 7) & 0xFF;
-    int flog2;
-    if (ebits != 0) {
-        flog2 = ebits - 127;
-    } else {
-        int m = (int)(amax_bits & 0x7F);               // subnormal: m * 2^-133
-        flog2 = (31 - __clz(m)) - 133;
-    }
-    int e = flog2 - 8;
-    return e < -127 ? -127 : (e > 127 ? 127 : e);
-}
-
-// 2^k as an fp32 value for k in [-149, 127] (exact).
-__device__ __forceinline__ float exp2i(int k) {
-    if (k >= -126) return __uint_as_float((uint32_t)(k + 127) << 23);
-    return __uint_as_float(1u << (k + 149));
-}
-
 // Block-wide max of a 32-bit pattern (all threads get the result).
 __device__ __forceinline__ uint32_t block_max_u32(uint32_t v, uint32_t* red /* [32] */) {
 #pragma unroll

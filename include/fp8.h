@@ -345,6 +345,81 @@ FP8_API int32_t fp8_linear_forward_noalloc(const void* x_dev, int64_t M, int64_t
                                            int32_t w_fmt, int64_t N, void* y_dev, int64_t ldy,
                                            int32_t* dev_status, void* stream);
 
+/*
+ * Activation and residual in the GEMM epilogue: with v the fp32 scaled accumulator of
+ * fp8_scaled_gemm,
+ *   v' = act(v + bias[n]) + residual[m, n]        (all in fp32)
+ *   y  = bf16_RNE(v')
+ * and then y, amax and yq as described with fp8_epilogue_t (whose options `base` holds).
+ *   activation    GELU = v Phi(v) (erf form); GELU_TANH = its tanh approximation
+ *                 0.5 v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))); SILU = v / (1 + exp(-v)).
+ *   residual_dev  nullable bf16 [M, N], row stride ldres >= N, 2-byte aligned (fastest with
+ *                 ldres % 8 == 0 and a 16-byte aligned base).  It may be y_dev itself
+ *                 (same address and stride: y is then accumulated into); otherwise it must
+ *                 not overlap any output.
+ * NULL, or a descriptor with nothing set, is plain fp8_scaled_gemm.
+ */
+typedef enum {
+    FP8_ACT_NONE = 0,
+    FP8_ACT_RELU = 1,
+    FP8_ACT_GELU = 2,
+    FP8_ACT_GELU_TANH = 3,
+    FP8_ACT_SILU = 4
+} fp8_activation_t;
+
+typedef struct {
+    fp8_epilogue_t base;
+    int32_t activation;
+    const void* residual_dev;
+    int64_t ldres;
+} fp8_epilogue_act_t;
+
+/* fp8_scaled_gemm with bias, activation, residual and the options of fp8_epilogue_t. */
+FP8_API int32_t fp8_scaled_gemm_act(const uint8_t* a_dev, const void* a_scale_dev, int32_t a_mode, int32_t fmt_a,
+                                    const uint8_t* b_dev, const void* b_scale_dev, int32_t b_mode, int32_t fmt_b,
+                                    int64_t M, int64_t N, int64_t K, void* y_dev, int64_t ldy,
+                                    const fp8_epilogue_act_t* epi, int32_t* dev_status, void* workspace_dev,
+                                    size_t ws_bytes, void* stream);
+
+/* fp8_linear_forward with the same epilogue. */
+FP8_API int32_t fp8_linear_forward_act(const void* x_dev, int64_t M, int64_t K, int64_t ldx, int32_t x_fmt,
+                                       int32_t x_mode, fp8_history_t* hist,
+                                       const uint8_t* w_dev, const void* w_scale_dev, int32_t w_mode,
+                                       int32_t w_fmt, int64_t N, void* y_dev, int64_t ldy,
+                                       const fp8_epilogue_act_t* epi, int32_t* dev_status,
+                                       void* workspace_dev, size_t ws_bytes, void* stream);
+
+/*
+ * fp8_rmsnorm_quantize -- residual addition, root-mean-square norm and FP8 output in one
+ * pass over the rows: what stands in front of an FP8 linear.  In fp32, per row:
+ *   h = x + residual                       (residual_dev != NULL; else h = x)
+ *   y = h / sqrt(mean(h^2) + eps) * weight
+ *   (q, scale) = y quantised as fp8_quantize does its input (amax over y's groups)
+ * and each output is rounded once, from the fp32 values: sum_dev = bf16_RNE(h),
+ * y_dev = bf16_RNE(y), the codes from y itself (not from its bf16 rounding).
+ *   x_dev        bf16 [rows, cols], row stride ldx.  residual_dev, sum_dev: the same with
+ *                ldr, lds.  All 16-byte aligned with strides % 8 == 0.
+ *   residual_dev nullable.  sum_dev nullable (needs residual_dev); may be x_dev or
+ *                residual_dev itself (same address and stride).
+ *   weight_dev   nullable bf16 [cols], 16-byte aligned (NULL: 1).   eps  finite, > 0.
+ *   cols         % 16 == 0 (% 32 for MX32), <= FP8_RMSNORM_MAX_COLS.  rows >= 0.
+ *   fmt, mode    ROW, BLOCK_1x128, MX32 (E4M3 only), or TENSOR with the scale of a given
+ *                amax (*amax_dev, as fp8_quantize_with_amax; the current or delayed
+ *                scale of the whole tensor would need a pass of its own).
+ *   amax_dev     TENSOR only (else NULL): device float >= 0.
+ *   q_dev        uint8 [rows, cols] dense, 16-byte aligned; scale_dev as fp8_quantize.
+ *   y_dev        nullable bf16 [rows, cols] dense, 16-byte aligned.
+ *   dev_status   nullable; FP8_ERR_NONFINITE when a row's y holds a NaN/Inf (that row's
+ *                outputs are then unspecified, other rows' are not).
+ * No workspace.  Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA.
+ */
+#define FP8_RMSNORM_MAX_COLS 32768
+FP8_API int32_t fp8_rmsnorm_quantize(const void* x_dev, int64_t rows, int64_t cols, int64_t ldx,
+                                     const void* residual_dev, int64_t ldr, void* sum_dev, int64_t lds,
+                                     const void* weight_dev, float eps, int32_t fmt, int32_t mode,
+                                     const float* amax_dev, uint8_t* q_dev, void* scale_dev, void* y_dev,
+                                     int32_t* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
