@@ -14,7 +14,8 @@ import importlib
 
 __all__ = ["fp8_abi_version", "fp8_status_string", "fp8_device_check", "fp8_workspace_size", "fp8_quantize",
            "fp8_scaled_gemm", "fp8_linear_forward", "fp8_amax", "fp8_quantize_with_amax", "fp8_scaled_gemm_ex",
-           "fp8_linear_forward_ex", "fp8_weight_only_linear", "History", "FP8Error", "binding", "inputs"]
+           "fp8_linear_forward_ex", "fp8_weight_only_linear", "fp8_scaled_gemm_act", "fp8_linear_forward_act",
+           "fp8_rmsnorm_quantize", "fp8_kv_append", "fp8_kv_attention", "KVCache", "History", "FP8Error", "binding", "inputs"]
 
 
 def __getattr__(name):

@@ -33,6 +33,7 @@ EXPORTED = ("fp8_abi_version", "fp8_status_string", "fp8_device_check", "fp8_wor
             "fp8_quantize", "fp8_scaled_gemm", "fp8_linear_forward", "fp8_linear_forward_noalloc",
             "fp8_amax", "fp8_quantize_with_amax", "fp8_scaled_gemm_ex", "fp8_linear_forward_ex",
             "fp8_weight_only_linear", "fp8_scaled_gemm_act", "fp8_linear_forward_act", "fp8_rmsnorm_quantize",
+            "fp8_kv_append", "fp8_kv_attention", "fp8_kv_attention_workspace_size",
             "fp8_testing_set_wait_limit_ns", "fp8_testing_encode_f32_range")
 FP8_WEIGHT_ONLY_MAX_TOKENS = 64
 FP8_NOALLOC_SCRATCH_BYTES = 4194304
@@ -53,6 +54,14 @@ class fp8_epilogue_t(ctypes.Structure):
 class fp8_epilogue_act_t(ctypes.Structure):
     _fields_ = [("base", fp8_epilogue_t), ("activation", ctypes.c_int32), ("residual_dev", ctypes.c_void_p),
                 ("ldres", ctypes.c_int64)]
+
+
+class fp8_kv_cache_t(ctypes.Structure):
+    _fields_ = [("k_dev", ctypes.c_void_p), ("v_dev", ctypes.c_void_p), ("k_scale_dev", ctypes.c_void_p),
+                ("v_scale_dev", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("fmt", ctypes.c_int32),
+                ("page_table_dev", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("kv_lens_dev", ctypes.c_void_p), ("batch", ctypes.c_int32)]
 
 
 _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
@@ -91,6 +100,13 @@ _lib.fp8_linear_forward_act.argtypes = [_P, _I64, _I64, _I64, _I32, _I32, ctypes
 _lib.fp8_rmsnorm_quantize.restype = _I32
 _lib.fp8_rmsnorm_quantize.argtypes = [_P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, ctypes.c_float, _I32, _I32, _P, _P,
                                       _P, _P, _P, _P]
+_lib.fp8_kv_append.restype = _I32
+_lib.fp8_kv_append.argtypes = [ctypes.POINTER(fp8_kv_cache_t), _P, _I64, _P, _I64, _I64, _P, _I32, _P, _P]
+_lib.fp8_kv_attention_workspace_size.restype = _SZ
+_lib.fp8_kv_attention_workspace_size.argtypes = [_I32, _I32, _I32, _I32, _I32, _I64]
+_lib.fp8_kv_attention.restype = _I32
+_lib.fp8_kv_attention.argtypes = [ctypes.POINTER(fp8_kv_cache_t), _P, _I64, _I32, _I64, _P, _I32, _I64, ctypes.c_float,
+                                  _P, _I64, _P, _P, _SZ, _P]
 _lib.fp8_weight_only_linear.restype = _I32
 _lib.fp8_weight_only_linear.argtypes = [_P, _I64, _I64, _I64, _P, _P, _I32, _I32, _I64, _P, _I64, _P, _P]
 _lib.fp8_testing_set_wait_limit_ns.restype = None
@@ -370,6 +386,97 @@ def fp8_rmsnorm_quantize(x, weight, eps, fmt, mode, q, scale, *, residual=None, 
                                    float(eps), fmt, mode, _ptr(amax), _ptr(q), _ptr(scale), _ptr(y), _ptr(dev_status),
                                    _stream(stream))
     _check(rc, "fp8_rmsnorm_quantize")
+
+
+class KVCache:
+    """A paged FP8 KV cache: uint8 codes k, v [num_pages, kv_heads, page_size, head_dim] and fp32 scales
+    k_scale, v_scale [num_pages, kv_heads], dense, kept by the caller."""
+
+    def __init__(self, k, v, k_scale, v_scale, fmt=FP8_E4M3):
+        for t in (k, v):
+            if t.dtype != torch.uint8 or t.dim() != 4 or t.shape != k.shape or not t.is_contiguous():
+                raise TypeError("k, v must be dense uint8 codes [num_pages, kv_heads, page_size, head_dim]")
+        for t in (k_scale, v_scale):
+            if t.dtype != torch.float32 or t.shape != k.shape[:2] or not t.is_contiguous():
+                raise TypeError("k_scale, v_scale must be dense fp32 [num_pages, kv_heads]")
+        self.k, self.v, self.k_scale, self.v_scale, self.fmt = k, v, k_scale, v_scale, fmt
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.c = fp8_kv_cache_t(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.num_pages,
+                                self.page_size, self.kv_heads, self.head_dim, fmt, None, 0, 0, None, 0)
+
+    @classmethod
+    def empty(cls, num_pages, kv_heads, page_size, head_dim, fmt=FP8_E4M3, device="cuda"):
+        """A cache with no tokens yet."""
+        shape = (num_pages, kv_heads, page_size, head_dim)
+        codes = [torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2)]
+        scales = [torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*codes, *scales, fmt)
+
+    def view(self, page_table, kv_lens):
+        """The C descriptor with a batch's page table [batch, max_pages] and lengths [batch] (int32)."""
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or (page_table.numel() and page_table.stride(1) != 1):
+            raise TypeError("page_table must be int32 [batch, max_pages] with unit column stride")
+        batch, pages = page_table.shape
+        if kv_lens.dtype != torch.int32 or kv_lens.dim() != 1 or kv_lens.shape[0] != batch or not kv_lens.is_contiguous():
+            raise TypeError("kv_lens must be int32 [batch]")
+        c = self.c
+        c.page_table_dev, c.max_pages = page_table.data_ptr(), pages
+        c.table_stride = page_table.stride(0) if batch > 1 and pages else pages
+        c.kv_lens_dev, c.batch = kv_lens.data_ptr(), batch
+        return c
+
+
+def _head_rows(t, name, heads, dim):
+    """Token stride of a bf16 [tokens, heads, dim] tensor whose heads are dense within a token."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or \
+            (t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim))):
+        raise TypeError(f"{name} must be bf16 [tokens, {heads}, {dim}], its heads dense within a token")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def _cu_q(cu_q, batch):
+    if cu_q is not None and (cu_q.dtype != torch.int32 or cu_q.dim() != 1 or cu_q.shape[0] != batch + 1
+                             or not cu_q.is_contiguous()):
+        raise TypeError("cu_q must be int32 [batch + 1]")
+    return _ptr(cu_q)
+
+
+def fp8_kv_append(k, v, cache: KVCache, page_table, kv_lens, *, cu_q=None, max_q_len=1, dev_status=None, stream=None):
+    """Quantize the new tokens' k, v (bf16 [tokens, kv_heads, head_dim]) into their pages: rows
+    [cu_q[b], cu_q[b + 1]) are the last tokens of sequence b, whose length with them is kv_lens[b]."""
+    ldk = _head_rows(k, "k", cache.kv_heads, cache.head_dim)
+    ldv = _head_rows(v, "v", cache.kv_heads, cache.head_dim)
+    if k.shape[0] != v.shape[0]:
+        raise TypeError("k and v must have as many tokens")
+    c = cache.view(page_table, kv_lens)
+    _check(_lib.fp8_kv_append(ctypes.byref(c), _ptr(k), ldk, _ptr(v), ldv, k.shape[0], _cu_q(cu_q, c.batch), max_q_len,
+                              _ptr(dev_status), _stream(stream)), "fp8_kv_append")
+
+
+def fp8_kv_attention_workspace_size(batch: int, q_heads: int, kv_heads: int, head_dim: int, max_q_len: int,
+                                    max_kv_len: int) -> int:
+    return _lib.fp8_kv_attention_workspace_size(batch, q_heads, kv_heads, head_dim, max_q_len, max_kv_len)
+
+
+def kv_attention_workspace(q, cache: KVCache, batch: int, max_q_len: int, max_kv_len: int):
+    """Workspace of fp8_kv_attention for q [tokens, q_heads, head_dim], or None when it needs none."""
+    n = fp8_kv_attention_workspace_size(batch, q.shape[1], cache.kv_heads, cache.head_dim, max_q_len, max_kv_len)
+    return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+
+
+def fp8_kv_attention(q, cache: KVCache, page_table, kv_lens, out, *, max_kv_len, cu_q=None, max_q_len=1,
+                     softmax_scale=None, workspace=None, dev_status=None, stream=None):
+    """Causal attention of q (bf16 [tokens, q_heads, head_dim]) over the cache into out (the same shape);
+    softmax_scale defaults to head_dim ** -0.5."""
+    if q.dim() != 3 or tuple(out.shape) != tuple(q.shape):
+        raise TypeError("q and out must be bf16 [tokens, q_heads, head_dim]")
+    ldq = _head_rows(q, "q", q.shape[1], cache.head_dim)
+    ldo = _head_rows(out, "out", q.shape[1], cache.head_dim)
+    c = cache.view(page_table, kv_lens)
+    scale = cache.head_dim ** -0.5 if softmax_scale is None else float(softmax_scale)
+    _check(_lib.fp8_kv_attention(ctypes.byref(c), _ptr(q), ldq, q.shape[1], q.shape[0], _cu_q(cu_q, c.batch), max_q_len,
+                                 max_kv_len, scale, _ptr(out), ldo, _ptr(dev_status), _ptr(workspace),
+                                 _nbytes(workspace), _stream(stream)), "fp8_kv_attention")
 
 
 def fp8_weight_only_linear(x, w, w_scale, w_mode, w_fmt, y, *, dev_status=None, stream=None):

@@ -233,6 +233,49 @@ int32_t gemm_impl(const uint8_t* a, const void* sa, int32_t am, int32_t fa, cons
     return cuda_status(launch_gemm(g, st));
 }
 
+// What fp8_kv_append and fp8_kv_attention have in common.
+int32_t check_kv(const fp8_kv_cache_t* c, int64_t tokens, const int32_t* cu_q, int32_t max_q) {
+    if (c == nullptr || (c->fmt != FP8_E4M3 && c->fmt != FP8_E5M2)) return FP8_ERR_INVALID_ARG;
+    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) return FP8_ERR_INVALID_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128) return FP8_ERR_INVALID_ARG;
+    if (c->kv_heads < 1 || c->kv_heads > 1024 || c->batch < 0 || c->batch > (1 << 20)) return FP8_ERR_INVALID_ARG;
+    if (c->num_pages < 0 || c->num_pages >= ((int64_t)1 << 31)) return FP8_ERR_INVALID_ARG;
+    if (c->max_pages < 0 || c->max_pages > c->table_stride) return FP8_ERR_INVALID_ARG;
+    if (tokens < 0 || tokens >= ((int64_t)1 << 31) || max_q < 0) return FP8_ERR_INVALID_ARG;
+    if (cu_q == nullptr && (tokens != c->batch || (max_q != 1 && c->batch > 0))) return FP8_ERR_INVALID_ARG;
+    if (tokens == 0 || c->batch == 0 || max_q == 0) return FP8_OK;      // nothing to do
+    if (!c->k_scale_dev || !c->v_scale_dev || !c->k_dev || !c->v_dev || !c->kv_lens_dev) return FP8_ERR_INVALID_ARG;
+    if (c->page_table_dev == nullptr && c->max_pages > 0) return FP8_ERR_INVALID_ARG;
+    if (!aligned16(c->k_dev) || !aligned16(c->v_dev)) return FP8_ERR_ALIGNMENT;
+    const uintptr_t words = reinterpret_cast<uintptr_t>(c->k_scale_dev) | reinterpret_cast<uintptr_t>(c->v_scale_dev) |
+                            reinterpret_cast<uintptr_t>(c->page_table_dev) | reinterpret_cast<uintptr_t>(c->kv_lens_dev) |
+                            reinterpret_cast<uintptr_t>(cu_q);
+    return (words & 3u) != 0 ? FP8_ERR_ALIGNMENT : FP8_OK;
+}
+
+KvArgs kv_args(const fp8_kv_cache_t* c, int64_t tokens, const int32_t* cu_q, int32_t max_q, int32_t* status) {
+    KvArgs a{};
+    a.k = c->k_dev;
+    a.v = c->v_dev;
+    a.k_scale = c->k_scale_dev;
+    a.v_scale = c->v_scale_dev;
+    a.num_pages = c->num_pages;
+    a.page_size = c->page_size;
+    a.kv_heads = c->kv_heads;
+    a.head_dim = c->head_dim;
+    a.fmt = c->fmt;
+    a.table = c->page_table_dev;
+    a.table_stride = c->table_stride;
+    a.max_pages = c->max_pages;
+    a.kv_lens = c->kv_lens_dev;
+    a.batch = c->batch;
+    a.cu_q = cu_q;
+    a.tokens = tokens;
+    a.max_q = max_q;
+    a.status = status;
+    return a;
+}
+
 // fp8_linear_forward with every epilogue option: quantise X into the workspace, then the GEMM.
 int32_t linear_impl(const void* x_dev, int64_t M, int64_t K, int64_t ldx, int32_t x_fmt, int32_t x_mode,
                     fp8_history_t* hist, const uint8_t* w_dev, const void* w_scale_dev, int32_t w_mode, int32_t w_fmt,
@@ -450,6 +493,65 @@ int32_t fp8_rmsnorm_quantize(const void* x_dev, int64_t rows, int64_t cols, int6
         return quantize_impl(x_dev, rows, cols, ldx, fmt, mode, q_dev, scale_dev, nullptr, nullptr, dev_status, nullptr, 0,
                              st);
     return cuda_status(launch_rmsnorm_quantize(a, st));
+}
+
+int32_t fp8_kv_append(const fp8_kv_cache_t* cache, const void* k_dev, int64_t ldk, const void* v_dev, int64_t ldv,
+                      int64_t tokens, const int32_t* cu_q_dev, int32_t max_q_len, int32_t* dev_status, void* stream) {
+    int32_t rc = check_kv(cache, tokens, cu_q_dev, max_q_len);
+    if (rc != FP8_OK) return rc;
+    const int64_t width = (int64_t)cache->kv_heads * cache->head_dim;
+    if (ldk < width || ldv < width) return FP8_ERR_INVALID_ARG;
+    const bool none = tokens == 0 || cache->batch == 0 || max_q_len == 0;
+    if (!none && (k_dev == nullptr || v_dev == nullptr)) return FP8_ERR_INVALID_ARG;
+    if (ldk % 8 != 0 || ldv % 8 != 0 || !aligned16(k_dev) || !aligned16(v_dev)) return FP8_ERR_ALIGNMENT;
+    if ((rc = device_gate()) != FP8_OK) return rc;
+    if (none) return FP8_OK;
+    return cuda_status(launch_kv_append(kv_args(cache, tokens, cu_q_dev, max_q_len, dev_status),
+                                        static_cast<const uint16_t*>(k_dev), ldk, static_cast<const uint16_t*>(v_dev),
+                                        ldv, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fp8_kv_attention_workspace_size(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                       int32_t max_q_len, int64_t max_kv_len) {
+    if (batch <= 0 || kv_heads <= 0 || q_heads <= 0 || q_heads % kv_heads != 0 || max_q_len <= 0 || max_kv_len <= 0 ||
+        (head_dim != 64 && head_dim != 128))
+        return 0;
+    return attention_workspace(batch, q_heads, kv_heads, head_dim, max_q_len, max_kv_len);
+}
+
+int32_t fp8_kv_attention(const fp8_kv_cache_t* cache, const void* q_dev, int64_t ldq, int32_t q_heads, int64_t tokens,
+                         const int32_t* cu_q_dev, int32_t max_q_len, int64_t max_kv_len, float softmax_scale,
+                         void* out_dev, int64_t ldo, int32_t* dev_status, void* workspace_dev, size_t ws_bytes,
+                         void* stream) {
+    int32_t rc = check_kv(cache, tokens, cu_q_dev, max_q_len);
+    if (rc != FP8_OK) return rc;
+    if (q_heads < 1 || q_heads % cache->kv_heads != 0 || q_heads > (1 << 16)) return FP8_ERR_INVALID_ARG;
+    const int64_t width = (int64_t)q_heads * cache->head_dim;
+    if (ldq < width || ldo < width) return FP8_ERR_INVALID_ARG;
+    if (max_kv_len < 0 || max_kv_len >= ((int64_t)1 << 30) || max_q_len >= (1 << 24)) return FP8_ERR_INVALID_ARG;
+    if (!(softmax_scale >= -3.402823466e38f && softmax_scale <= 3.402823466e38f)) return FP8_ERR_INVALID_ARG;
+    const bool none = tokens == 0 || cache->batch == 0 || max_q_len == 0;
+    if (!none && (q_dev == nullptr || out_dev == nullptr)) return FP8_ERR_INVALID_ARG;
+    if (ldq % 8 != 0 || ldo % 8 != 0 || !aligned16(q_dev) || !aligned16(out_dev)) return FP8_ERR_ALIGNMENT;
+    const size_t need = fp8_kv_attention_workspace_size(cache->batch, q_heads, cache->kv_heads, cache->head_dim,
+                                                        max_q_len, max_kv_len);
+    if (need > 0 && !none) {
+        if (workspace_dev == nullptr || ws_bytes < need) return FP8_ERR_WORKSPACE;
+        if (!aligned16(workspace_dev)) return FP8_ERR_ALIGNMENT;
+    }
+    if ((rc = device_gate()) != FP8_OK) return rc;
+    if (none) return FP8_OK;
+    AttnArgs a{};
+    a.c = kv_args(cache, tokens, cu_q_dev, max_q_len, dev_status);
+    a.q = static_cast<const uint16_t*>(q_dev);
+    a.ldq = ldq;
+    a.q_heads = q_heads;
+    a.max_kv = max_kv_len;
+    a.softmax_scale = softmax_scale;
+    a.out = static_cast<uint16_t*>(out_dev);
+    a.ldo = ldo;
+    a.workspace = workspace_dev;
+    return cuda_status(launch_kv_attention(a, static_cast<cudaStream_t>(stream)));
 }
 
 int32_t fp8_weight_only_linear(const void* x_dev, int64_t M, int64_t K, int64_t ldx, const uint8_t* w_dev,

@@ -116,4 +116,39 @@ struct NormArgs {            // residual + RMSNorm + FP8 output (norm.cu)
 };
 cudaError_t launch_rmsnorm_quantize(const NormArgs& a, cudaStream_t st);
 
+struct KvArgs {              // the paged FP8 cache and the call's tokens (kv_cache.cu, attention.cu)
+    uint8_t* k;              // codes [num_pages][kv_heads][page_size][head_dim]
+    uint8_t* v;
+    float* k_scale;          // [num_pages][kv_heads]
+    float* v_scale;
+    int64_t num_pages;
+    int32_t page_size, kv_heads, head_dim, fmt;
+    const int32_t* table;    // [batch][table_stride]
+    int64_t table_stride, max_pages;
+    const int32_t* kv_lens;
+    int32_t batch;
+    const int32_t* cu_q;     // [batch + 1], or null: one token per sequence
+    int64_t tokens;
+    int32_t max_q;
+    int32_t* status;
+};
+cudaError_t launch_kv_append(const KvArgs& c, const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                             cudaStream_t st);
+
+struct AttnArgs {
+    KvArgs c;
+    const uint16_t* q;       // bf16 [tokens][q_heads][head_dim], token stride ldq
+    int64_t ldq;
+    int32_t q_heads;
+    int64_t max_kv;
+    float softmax_scale;
+    uint16_t* out;
+    int64_t ldo;
+    void* workspace;
+};
+// How a call's work is split: row tiles per (sequence, KV head) and splits of the cached tokens.
+size_t attention_workspace(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t max_q,
+                           int64_t max_kv);
+cudaError_t launch_kv_attention(const AttnArgs& a, cudaStream_t st);
+
 }  // namespace fp8b

@@ -420,6 +420,95 @@ FP8_API int32_t fp8_rmsnorm_quantize(const void* x_dev, int64_t rows, int64_t co
                                      const float* amax_dev, uint8_t* q_dev, void* scale_dev, void* y_dev,
                                      int32_t* dev_status, void* stream);
 
+/*
+ * A paged FP8 KV cache and one batch's view of it.  (The pages name an FP8 KV cache but give
+ * no layout; this one is the library's own.)
+ *   k_dev, v_dev     uint8 codes [num_pages][kv_heads][page_size][head_dim] of format fmt
+ *                    (E4M3 or E5M2), 16-byte aligned.
+ *   k_scale_dev, v_scale_dev  float [num_pages][kv_heads]: one dequantisation multiplier per
+ *                    page and KV head, positive and finite.  fp8_kv_append writes powers of
+ *                    two.
+ *   page_size        16, 32, 64 or 128 tokens.   head_dim  64 or 128.
+ *   page_table_dev   int32 [batch][table_stride]: entry i of row b is the page of the tokens
+ *                    [i page_size, (i + 1) page_size) of sequence b; max_pages <= table_stride
+ *                    entries of a row may be read (only those that the sequence's length
+ *                    reaches are).
+ *   kv_lens_dev      int32 [batch]: tokens of each sequence in the cache, those of the
+ *                    present call included: both calls below read the same array.
+ *   batch            sequences, >= 0.
+ * The tokens of one call: rows [cu_q[b], cu_q[b + 1]) of the call's bf16 tensors belong to
+ * sequence b and are its last tokens, at positions kv_lens[b] - (cu_q[b + 1] - cu_q[b]) and
+ * up.  cu_q_dev is int32 [batch + 1], non-decreasing; NULL means one token per sequence
+ * (row b).  max_q_len bounds the tokens of one sequence.  Rows at or past cu_q[batch] are
+ * neither read nor written.
+ * What only the device sees is checked there: a sequence with a bad cu_q, with more tokens
+ * than max_q_len or than its page-table row or max_kv_len allows, or a page index outside
+ * [0, num_pages) sets FP8_ERR_INVALID_ARG in dev_status; nothing is then read or written for
+ * that sequence or page (fp8_kv_attention: those outputs are unspecified).
+ */
+typedef struct {
+    uint8_t* k_dev;
+    uint8_t* v_dev;
+    float* k_scale_dev;
+    float* v_scale_dev;
+    int64_t num_pages;
+    int32_t page_size, kv_heads, head_dim, fmt;
+    const int32_t* page_table_dev;
+    int64_t table_stride, max_pages;
+    const int32_t* kv_lens_dev;
+    int32_t batch;
+} fp8_kv_cache_t;
+
+/*
+ * fp8_kv_append -- quantises the new tokens' K and V into their pages.  Per page and KV head:
+ *   s_new = 2^e, the least e with max(amax, 1e-12) <= F_max 2^e, amax = max |x| of the
+ *           call's tokens in that page
+ *   s     = s_new                  when the call fills the page from its first token
+ *         = max(s_old, s_new)      when the page held earlier tokens of the sequence; their
+ *                                  codes become RNE(decode(q) s_old / s)
+ *   q     = RNE(x / s)
+ * FP8 codes carry their own exponent, so a power-of-two scale loses no precision, and a page
+ * whose scale grows keeps its earlier codes' values except where they become subnormal.
+ * Slots of a page that hold no token are left as they were.
+ *   k_dev, v_dev  bf16 [tokens][kv_heads][head_dim], token strides ldk / ldv elements
+ *                 (% 8 == 0, >= kv_heads head_dim), 16-byte aligned: two parts of one
+ *                 projection's rows will do.
+ *   tokens        rows of k_dev / v_dev (== batch when cu_q_dev is NULL).
+ *   dev_status    nullable; FP8_ERR_NONFINITE for a NaN/Inf element (that page and head are
+ *                 then unspecified), FP8_ERR_INVALID_ARG as above.
+ * No two sequences of a call may append to one page (pages that sequences share are full).
+ * No workspace.  Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA.
+ */
+FP8_API int32_t fp8_kv_append(const fp8_kv_cache_t* cache, const void* k_dev, int64_t ldk, const void* v_dev,
+                              int64_t ldv, int64_t tokens, const int32_t* cu_q_dev, int32_t max_q_len,
+                              int32_t* dev_status, void* stream);
+
+/*
+ * fp8_kv_attention -- causal attention of bf16 queries over the cache:
+ *   out[t, h] = sum_j p_j v_j,  p = softmax_j(softmax_scale q[t, h] . k_j)
+ * over the tokens j of the query's sequence up to and including its own position, k_j and v_j
+ * the dequantised cache (decode(code) scale) of KV head h / (q_heads / kv_heads).  The codes
+ * are decoded on chip (exactly); scores, softmax and sums are in fp32, the products' operands
+ * in fp16 (codes exactly; a query row after a power-of-two normalisation; the weights p),
+ * out is rounded once to bf16.  A query that sees no token (kv_len 0) gives zeros.
+ *   q_dev, out_dev  bf16 [tokens][q_heads][head_dim], token strides ldq / ldo (% 8 == 0,
+ *                   >= q_heads head_dim), 16-byte aligned.
+ *   q_heads         a multiple of kv_heads.
+ *   max_kv_len      bounds every kv_lens[b].  It and max_q_len size the launch.
+ *   softmax_scale   finite.
+ *   workspace       fp8_kv_attention_workspace_size bytes, 16-byte aligned, needs no
+ *                   initialisation; calls that share one must not overlap on the GPU.
+ * The result does not depend on the batch's other sequences' contents, and is the same from
+ * run to run for the same sizes.  Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE,
+ * WORKSPACE, CUDA.
+ */
+FP8_API size_t fp8_kv_attention_workspace_size(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                               int32_t max_q_len, int64_t max_kv_len);
+FP8_API int32_t fp8_kv_attention(const fp8_kv_cache_t* cache, const void* q_dev, int64_t ldq, int32_t q_heads,
+                                 int64_t tokens, const int32_t* cu_q_dev, int32_t max_q_len, int64_t max_kv_len,
+                                 float softmax_scale, void* out_dev, int64_t ldo, int32_t* dev_status,
+                                 void* workspace_dev, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -71,3 +71,73 @@ def test_binding_type_checks():
     for res in (y.float(), y[:3], torch.empty((8, 4), dtype=torch.bfloat16).t()):
         with pytest.raises(TypeError):
             b.fp8_scaled_gemm_act(a, s, 1, 0, w, s, 1, 0, y, residual=res)
+
+
+def kv_cache(**kw):
+    d = dict(k_dev=P, v_dev=P, k_scale_dev=P, v_scale_dev=P, num_pages=4, page_size=16, kv_heads=2, head_dim=64, fmt=0,
+             page_table_dev=P, table_stride=4, max_pages=4, kv_lens_dev=P, batch=2) | kw
+    return b.fp8_kv_cache_t(**d)
+
+
+def append(k=P, ldk=128, v=P, ldv=128, tokens=2, cu=None, max_q=1, **kw):
+    return L.fp8_kv_append(ctypes.byref(kv_cache(**kw)), k, ldk, v, ldv, tokens, cu, max_q, None, None)
+
+
+def attend(q=P, ldq=256, heads=4, tokens=2, cu=None, max_q=1, max_kv=64, scale=0.1, out=P, ldo=256, ws=P, ws_bytes=1 << 30,
+           **kw):
+    return L.fp8_kv_attention(ctypes.byref(kv_cache(**kw)), q, ldq, heads, tokens, cu, max_q, max_kv, scale, out, ldo, None,
+                              ws, ws_bytes, None)
+
+
+BAD_CACHE = [dict(fmt=2), dict(page_size=48), dict(page_size=0), dict(page_size=256), dict(head_dim=96),
+             dict(head_dim=256), dict(kv_heads=0), dict(batch=-1), dict(num_pages=-1), dict(max_pages=5), dict(max_pages=-1),
+             dict(k_dev=None), dict(v_scale_dev=None), dict(kv_lens_dev=None), dict(page_table_dev=None), dict(tokens=-1),
+             dict(max_q=-1), dict(tokens=3), dict(max_q=2)]
+
+
+@pytest.mark.parametrize("kw", BAD_CACHE)
+def test_kv_cache_refusals(kw):
+    assert append(**kw) == INV
+    assert attend(**kw) == INV
+
+
+def test_kv_append_refusals():
+    assert L.fp8_kv_append(None, P, 128, P, 128, 2, None, 1, None, None) == INV
+    for kw in (dict(ldk=120), dict(ldv=64), dict(k=None), dict(v=None)):
+        assert append(**kw) == INV
+    for kw in (dict(ldk=132), dict(k=P + 2), dict(v=P + 8), dict(k_dev=P + 8), dict(v_scale_dev=P + 2),
+               dict(kv_lens_dev=P + 1), dict(cu=P + 2, max_q=5)):
+        assert append(**kw) == ALIGN
+
+
+def test_kv_attention_refusals():
+    for kw in (dict(heads=3), dict(heads=0), dict(ldq=248), dict(ldo=248), dict(q=None), dict(out=None), dict(max_kv=-1),
+               dict(max_kv=1 << 30), dict(scale=float("nan")), dict(scale=float("inf")), dict(max_q=1 << 24, cu=P)):
+        assert attend(**kw) == INV
+    for kw in (dict(q=P + 2), dict(ldq=260), dict(out=P + 8), dict(ldo=260), dict(ws=P + 4, max_kv=100000)):
+        assert attend(**kw) == ALIGN
+    n = b.fp8_kv_attention_workspace_size(2, 4, 2, 64, 1, 100000)
+    assert n > 0
+    assert attend(max_kv=100000, ws=None) == b.FP8_ERR_WORKSPACE
+    assert attend(max_kv=100000, ws_bytes=n - 1) == b.FP8_ERR_WORKSPACE
+    for bad in ((0, 4, 2, 64, 1, 10), (1, 4, 3, 64, 1, 10), (1, 4, 2, 96, 1, 10), (1, 4, 2, 64, 0, 10), (1, 4, 2, 64, 1, 0)):
+        assert b.fp8_kv_attention_workspace_size(*bad) == 0
+
+
+def test_kv_binding_type_checks():
+    cache = b.KVCache.empty(4, 2, 16, 64, device="cpu")
+    table, lens = torch.zeros((2, 3), dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    x = torch.empty((2, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        b.KVCache(cache.k[:, :, :, :32], cache.v, cache.k_scale, cache.v_scale)
+    with pytest.raises(TypeError):
+        b.KVCache(cache.k, cache.v, cache.k_scale.double(), cache.v_scale)
+    for k, v, t, n in ((x.float(), x, table, lens), (x[:1], x, table, lens), (x, x.transpose(0, 1), table.long(), lens),
+                       (x, x, table, lens[:1]), (x[:, :1], x, table, lens), (x.transpose(0, 1).contiguous().transpose(0, 1), x,
+                                                                              table, lens)):
+        with pytest.raises(TypeError):
+            b.fp8_kv_append(k, v, cache, t, n)
+    with pytest.raises(TypeError):
+        b.fp8_kv_append(x, x, cache, table, lens, cu_q=torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        b.fp8_kv_attention(x, cache, table, lens, x[:1], max_kv_len=16)
