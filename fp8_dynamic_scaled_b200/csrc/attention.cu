@@ -3,29 +3,54 @@
 //   out[t, h] = sum_j p_j v_j,  p = softmax_j(scale q[t, h] . k_j),  j up to t's own position
 //
 // One pass over the cached tokens with a running maximum and sum.  The heads that share a KV
-// head are rows of one tile (rows = query tokens x group), so that a page is read once for
-// all of them.  Operands of the products are fp16: FP8 codes are fp16 values (no rounding);
+// head are rows of one tile (rows = query tokens x group, 8 or 16 of them), so that a page is read
+// once for all of them.  Operands of the products are fp16: FP8 codes are fp16 values (no rounding);
 // a query row is first divided by a power of two so that its largest element is in [1, 2); the
-// weights p are at most 2^15, so that fp16 keeps 11 bits of a weight down to 2^-29 of the
-// largest.  Scores, softmax statistics and sums are fp32.
+// weights are scaled to 2^8 .. 2^15 for the largest, so that fp16 keeps 11 bits of a weight
+// down to 2^-22 of it.  Scores, softmax statistics and sums are fp32.
 //
 // The page's scales: with z = scale q . code_k * s_k in units of log2, the running maximum M is
-// taken over z + log2 s_v, and the weight is w = 2^(z + log2 s_v - M + 15): sum w code_v is then
+// taken over z + log2 s_v, and the weight is w = 2^(z + log2 s_v - M + 8): sum w code_v is then
 // sum p v without a product per page, whatever the spread of s_v among pages, and the sum of
-// the softmax is sum w / s_v.
+// the softmax is sum w / s_v.  M may lag behind the true maximum by 2^7, which fp16 has room
+// for: the sums are moved to a new M only when a score passes that, a rare event after the
+// first tiles.
+#include "gemm_common.cuh"
 #include "kv_common.cuh"
 
 namespace fp8b {
 
 namespace {
 
-constexpr int A_WARPS = 4;
-constexpr int A_THREADS = 32 * A_WARPS;
-constexpr int A_ROWS = 16;            // rows of a tile (mma m16)
-constexpr int A_STEP = 32;            // tokens per warp and iteration
-constexpr int A_CTA_STEP = A_STEP * A_WARPS;
+constexpr int A_TOK = 32;             // tokens of a work tile: one ring stage, one warp
+constexpr int A_HEADER = 1024;        // barriers, the CTA's place in the work
+constexpr int A_MAX_STAGES = 24;
+constexpr int A_SMEM = 227 * 1024;
+
+// 8 or 16 rows per tile (NQ = 1, 2).  With 8 the accumulators leave room for 16 warps per SM (128
+// registers), with 16 for 12 (168 registers).
+template <int D, int NQ>
+struct Shape {
+    static constexpr int ROWS = 8 * NQ;
+    static constexpr int WARPS = NQ == 1 ? 10 : 8;                  // consumers
+    static constexpr int PRODUCERS = NQ == 1 ? 4 : 2;               // warps that fill the ring
+    static constexpr int THREADS = 32 * (WARPS + PRODUCERS + 1);    // and the joining warp
+    static constexpr int LD = D + 4;                                // floats per row of a warp's part
+    static constexpr int PART_BYTES = WARPS * ROWS * LD * 4;
+    static constexpr int ML_BYTES = WARPS * ROWS * 8;
+    static constexpr int STAGE = 2 * A_TOK * D;
+    static constexpr int FIT = (A_SMEM - 1024 - A_HEADER - PART_BYTES - ML_BYTES - A_MAX_STAGES * 32) / STAGE;
+    // Every stage belongs to one producer and one consumer.  A warp then sees each phase of its
+    // stages' barriers in turn; a consumer that shared its stages with others could ask for a
+    // phase while the barrier is two phases behind, which a parity cannot tell from done.
+    static constexpr int TURN = NQ == 1 ? 20 : 8;
+    static constexpr int STAGES = (FIT < A_MAX_STAGES ? FIT : A_MAX_STAGES) / TURN * TURN;
+    static_assert(TURN % WARPS == 0 && TURN % PRODUCERS == 0 && STAGES > 0, "stages have one owner on each side");
+};
+
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr float P_SHIFT = 15.0f;
+constexpr float P_SHIFT = 8.0f;        // the largest weight is 2^8 ..
+constexpr float P_LAG = 7.0f;          // .. to 2^15 (fp16 ends at 2^16)
 
 struct AttnParams {
     KvArgs c;
@@ -33,11 +58,13 @@ struct AttnParams {
     uint16_t* out;
     int64_t ldq, ldo, max_kv;
     int32_t q_heads, group;
-    int32_t row_tiles;                // per (sequence, KV head)
-    int32_t splits, chunk;            // tokens of one split (a multiple of A_CTA_STEP)
+    int32_t row_tiles;                // most row tiles of a (sequence, KV head)
+    int32_t box;                      // page rows of one copy: min(page_size, A_TOK)
     float scale2;                     // softmax_scale * log2(e)
-    float* part_o;                    // [units][splits][A_ROWS][D], unit = (b, head, row tile)
-    float2* part_ml;                  // [units][splits][A_ROWS]: maximum (log2), sum
+    float* part_o;                    // [2 grid][16][D]: a CTA's first and last part of a unit
+    float2* part_ml;                  // [2 grid][16]: maximum (log2), sum
+    int4* joins;                      // [grid]: the unit that begins in CTA i and goes on in the next
+    uint64_t wait_ns;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -51,408 +78,768 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Two codes (the low 16 bits) -> two fp16 values, exactly.
+// Four codes -> two pairs of fp16 values, exactly.
 template <int FMT>
-__device__ __forceinline__ uint32_t half2_of(uint32_t codes2) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes2 & 0xFFFFu),
-                                                    FMT == FP8_E4M3 ? __NV_E4M3 : __NV_E5M2);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+__device__ __forceinline__ void half2x2_of(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    if (FMT == FP8_E4M3)
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(codes));
+    else
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e5m2x2 %0, a;\n\t"
+            "cvt.rn.f16x2.e5m2x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(codes));
 }
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ float quad_max(float v) {
-    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-}
-__device__ __forceinline__ float quad_sum(float v) {
-    v += __shfl_xor_sync(0xffffffffu, v, 1);
-    return v + __shfl_xor_sync(0xffffffffu, v, 2);
+// The 8 x 8 block of 16-bit values that a warp holds in fragment layout, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
-// The rows of one tile and the tokens that they see together.
-struct Tile {
-    int32_t b, head, row0, rows;      // rows of the sequence and head in all
-    int32_t see;                      // tokens the last row of the tile sees
-    Sequence s;
+// ---------------------------------------------------------------- the work list
+// A unit is (sequence, KV head, row tile of 8 or 16 rows = query tokens x group); its work tiles
+// are 32 cached tokens each, up to the last token that one of its rows sees (one tile, without
+// tokens, when they see none).  The tiles of all units in a row are cut into equal ranges, one
+// for each CTA, whatever the lengths: a CTA works through the end of one unit, whole units
+// and the beginning of another.
+__device__ __forceinline__ int32_t rows_of(const AttnParams& p, const Sequence& s) { return s.ok ? s.n * p.group : 0; }
+
+// Tokens that row tile rt's last row sees.
+template <int ROWS>
+__device__ __forceinline__ int32_t tile_sees(const AttnParams& p, const Sequence& s, int32_t rt) {
+    const int32_t last = min((rt + 1) * ROWS, s.n * p.group) - 1;
+    return max(0, s.kv_len - s.n + last / p.group + 1);
+}
+__device__ __forceinline__ int32_t tiles_of(int32_t sees) { return max(1, (sees + A_TOK - 1) / A_TOK); }
+
+// Work tiles of one KV head of a sequence.
+template <int ROWS>
+__device__ __forceinline__ int64_t head_tiles(const AttnParams& p, const Sequence& s) {
+    const int32_t rts = (rows_of(p, s) + ROWS - 1) / ROWS;
+    int64_t n = 0;
+    for (int32_t rt = 0; rt < rts; ++rt) n += tiles_of(tile_sees<ROWS>(p, s, rt));
+    return n;
+}
+
+// This CTA's range of the work and where it begins: the whole CTA calls it.
+struct Range {
+    int64_t lo, total;
+    int32_t n;                        // tiles of the range
+    int32_t ctas;
+};
+struct Start {
+    int64_t inside;                   // tiles of sequence b before the range
+    int32_t b;
 };
 
-__device__ __forceinline__ Tile tile_of(const AttnParams& p, int32_t unit) {
-    Tile t;
-    const int32_t rt = unit % p.row_tiles, bh = unit / p.row_tiles;
-    t.head = bh % p.c.kv_heads;
-    t.b = bh / p.c.kv_heads;
-    t.s = sequence_of(p.c, t.b, p.max_kv);
-    t.row0 = rt * A_ROWS;
-    t.rows = t.s.n * p.group;
-    const int32_t last = min(t.row0 + A_ROWS, t.rows) - 1;
-    t.see = last >= t.row0 ? max(0, t.s.kv_len - t.s.n + last / p.group + 1) : 0;
-    return t;
+__device__ __forceinline__ int64_t range_begin(int64_t total, int32_t ctas, int32_t i) { return total * i / ctas; }
+
+template <class S>
+__device__ Range find_range(const AttnParams& p, Start* start, int64_t* sums /* [32] */) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = S::THREADS / 32;
+    const int32_t per = (p.c.batch + S::THREADS - 1) / S::THREADS;
+    const int32_t b0 = (int32_t)threadIdx.x * per, b1 = min(p.c.batch, b0 + per);
+    int64_t mine = 0;
+    for (int32_t b = b0; b < b1; ++b) {
+        const Sequence s = sequence_of(p.c, b, p.max_kv);
+        if (!s.ok && blockIdx.x == 0) report_status(p.c.status, FP8_ERR_INVALID_ARG);
+        mine += head_tiles<S::ROWS>(p, s) * p.c.kv_heads;
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    Range r;
+    int64_t before = 0;
+    r.total = 0;
+    for (int w = 0; w < nw; ++w) {
+        if (w < warp) before += sums[w];
+        r.total += sums[w];
+    }
+    // a CTA's warps share its tiles: fewer CTAs when there is not one tile for each warp
+    r.ctas = (int32_t)max((int64_t)1, min((int64_t)gridDim.x, (r.total + S::WARPS - 1) / S::WARPS));
+    const int32_t i = (int32_t)blockIdx.x;
+    r.lo = i < r.ctas ? range_begin(r.total, r.ctas, i) : r.total;
+    r.n = i < r.ctas ? (int32_t)(range_begin(r.total, r.ctas, i + 1) - r.lo) : 0;
+    const int64_t first = before + incl - mine;
+    if (r.lo >= first && r.lo < first + mine) {
+        int64_t at = first;
+        for (int32_t b = b0; b < b1; ++b) {
+            const int64_t n = head_tiles<S::ROWS>(p, sequence_of(p.c, b, p.max_kv)) * p.c.kv_heads;
+            if (r.lo < at + n) {
+                start->b = b;
+                start->inside = r.lo - at;
+                break;
+            }
+            at += n;
+        }
+    }
+    __syncthreads();
+    return r;
 }
 
-// ---------------------------------------------------------------- the split kernel
-// Fragment layouts (c = lane % 4, r = lane / 4).  QK: the reduction index is permuted so
-// that a lane's operands are 16 contiguous bytes of a token's K row: k-step kk takes the 4
-// codes at (kk / 4) * 64 + 16 c + 4 (kk % 4).  PV: n-tile j of the output holds
-// d = (D / 8) n + j, so that a lane's operands are D / 8 contiguous bytes of a V row.
-template <int FMT, int D>
-__global__ void __launch_bounds__(A_THREADS, 2) kv_attention_kernel(const __grid_constant__ AttnParams p) {
-    constexpr int KK = D / 16;                 // k-steps of QK = n-tiles of K's 16-byte chunks * 4
-    constexpr int NT = D / 8;                  // n-tiles of PV
-    constexpr int CH = D / 64;                 // 16-byte chunks of a K row per lane
-    __shared__ float so[A_WARPS][A_ROWS][D];
-    __shared__ float2 sml[A_WARPS][A_ROWS];
-    const int32_t unit = (int32_t)(blockIdx.x / p.splits), split = (int32_t)(blockIdx.x % p.splits);
-    const Tile t = tile_of(p, unit);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 3, r = lane >> 2;
-    if (!t.s.ok) {
-        if (split == 0 && threadIdx.x == 0) report_status(p.c.status, FP8_ERR_INVALID_ARG);
-        return;
-    }
-    if (t.row0 >= t.rows) return;
-    const int32_t begin = split * p.chunk, end = min(t.see, begin + p.chunk);
-    const int32_t used = max(1, (t.see + p.chunk - 1) / p.chunk);       // splits with tokens
-    if (split >= used) return;
-    const int32_t P = p.c.page_size;
-    // ---- the tile's rows: r and r + 8
-    int32_t limit[2];                           // tokens the row sees (0: a row beyond the last)
-    uint32_t qa[KK][4];
-    float qf[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int32_t row = t.row0 + r + 8 * i;
-        const bool real = row < t.rows;
-        const int32_t tok = real ? row / p.group : 0;
-        limit[i] = real ? max(0, t.s.kv_len - t.s.n + tok + 1) : 0;
-        const uint16_t* src = p.q + (int64_t)(t.s.first + tok) * p.ldq +
-                              (int64_t)(t.head * p.group + (real ? row % p.group : 0)) * D;
-        uint4 v[CH][2];
-        uint32_t m2 = 0;
-#pragma unroll
-        for (int h = 0; h < CH; ++h)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                v[h][e] = real ? ld_v4(src + h * 64 + 16 * c + 8 * e) : make_uint4(0, 0, 0, 0);
-                m2 = max_bf16x2_bits(m2, max_bf16x2_bits(max_bf16x2_bits(abs_bf16x2(v[h][e].x), abs_bf16x2(v[h][e].y)),
-                                                         max_bf16x2_bits(abs_bf16x2(v[h][e].z), abs_bf16x2(v[h][e].w))));
-            }
-        uint32_t m = hmax_pair(m2);
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const int e = max(1, min((int)(m >> 7), 253));                  // biased exponent of the row's largest
-        const float inv = __uint_as_float((uint32_t)(254 - e) << 23);   // 2^(127 - e)
-        qf[i] = __uint_as_float((uint32_t)e << 23) * p.scale2;
-#pragma unroll
-        for (int h = 0; h < CH; ++h)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t w0 = k < 2 ? (k == 0 ? v[h][0].x : v[h][0].z) : (k == 2 ? v[h][1].x : v[h][1].z);
-                const uint32_t w1 = k < 2 ? (k == 0 ? v[h][0].y : v[h][0].w) : (k == 2 ? v[h][1].y : v[h][1].w);
-                qa[4 * h + k][i] = pack_half2(bf16_lo(w0) * inv, bf16_hi(w0) * inv);
-                qa[4 * h + k][2 + i] = pack_half2(bf16_lo(w1) * inv, bf16_hi(w1) * inv);
-            }
-    }
-    const int32_t least = max(0, t.s.kv_len - t.s.n + t.row0 / p.group + 1);   // tokens the first row sees
-    float o[NT][4];
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
-    float mrow[2] = {-INFINITY, -INFINITY}, lrow[2] = {0.0f, 0.0f};
+// The unit at hand, walking through a range.
+template <int ROWS>
+struct Cursor {
+    int32_t b, h, rt, rts;
+    Sequence s;
+    int32_t sees, tiles;              // of the unit
 
-    // ---- pages: lane i holds the place of the 16 tokens i % 2 of iteration i / 2 of this warp
-    int32_t pages_at = -16;                     // first iteration that the lanes hold
-    int64_t place = -1;
-    float ksc = 0.0f, vsc = 0.0f;
-    const int32_t iters = end > begin ? (end - begin + A_CTA_STEP - 1) / A_CTA_STEP : 0;
-    auto hold = [&](int32_t it) {
-        if (it < pages_at + 16) return;
-        pages_at = it;
-        const int32_t tok = begin + (it + (lane >> 1)) * A_CTA_STEP + warp * A_STEP + (lane & 1) * 16;
-        place = -1;
-        ksc = vsc = 1.0f;
-        if (tok < end) {
-            const int32_t page = __ldg(p.c.table + (int64_t)t.b * p.c.table_stride + tok / P);
-            if (page >= 0 && page < p.c.num_pages) {
-                const int64_t at = (int64_t)page * p.c.kv_heads + t.head;
-                place = (at * P + tok % P) * D;
-                ksc = __ldg(p.c.k_scale + at);
-                vsc = __ldg(p.c.v_scale + at);
-            } else {
-                report_status(p.c.status, FP8_ERR_INVALID_ARG);
+    __device__ __forceinline__ void unit(const AttnParams& p) {
+        sees = tile_sees<ROWS>(p, s, rt);
+        tiles = tiles_of(sees);
+    }
+    __device__ __forceinline__ void sequence(const AttnParams& p, int32_t b0) {
+        b = b0;
+        s = sequence_of(p.c, b, p.max_kv);
+        rts = (rows_of(p, s) + ROWS - 1) / ROWS;
+        h = rt = 0;
+    }
+    __device__ __forceinline__ void next(const AttnParams& p) {
+        if (++rt == rts) {
+            rt = 0;
+            if (++h == p.c.kv_heads) {
+                do { sequence(p, b + 1); } while (rts == 0 && b + 1 < p.c.batch);
             }
         }
-    };
-    uint4 kb[4][CH];                            // K of 32 tokens: token 8 i + r, chunks
-    uint2 vb[8][NT / 8];                        // V of 32 tokens: 16 (i / 4) + {2c, 2c+1, 2c+8, 2c+9}[i % 4]
-    auto load_k = [&](int32_t it) {
+        unit(p);
+    }
+    // The unit of the range's first tile; returns the tiles of that unit before the range.
+    __device__ __forceinline__ int32_t open(const AttnParams& p, const Start& st) {
+        sequence(p, st.b);
+        int64_t inside = st.inside;
+        const int64_t per_head = head_tiles<ROWS>(p, s);
+        h = (int32_t)(inside / per_head);
+        inside -= h * per_head;
+        unit(p);
+        while (inside >= tiles) {
+            inside -= tiles;
+            ++rt;
+            unit(p);
+        }
+        return (int32_t)inside;
+    }
+};
+
+// ---------------------------------------------------------------- the ring
+// One stage: 32 tokens of K, then of V, D bytes each, as TMA wrote them (128-byte rows with the
+// 128-byte swizzle, or 64-byte rows with the 64-byte one), and the tile's numbers.
+struct __align__(16) StageInfo {
+    float ks[2], lv[2], iv[2];        // per 16 tokens: s_k, log2 s_v + P_SHIFT, 1 / s_v
+    int32_t valid[2];                 // tokens of the 16 that are there
+};
+
+template <int D>
+__device__ __forceinline__ uint32_t stage_chunk(uint32_t row, uint32_t chunk) {   // byte offset of 16 bytes
+    return D == 128 ? row * 128 + ((chunk ^ (row & 7)) << 4) : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
+}
+
+struct Ring {
+    uint8_t* data;
+    StageInfo* info;
+    uint64_t *full, *empty;
+    volatile int32_t* abort_flag;
+};
+
+// The range's tile g sits in stage g % STAGES; it is fetched by producer g % PRODUCERS and used
+// by consumer g % WARPS.  (One producer warp could not keep up: a tile costs it about 700
+// cycles, and at HBM's rate an SM takes one every 350.)
+template <int D, class S>
+__device__ __forceinline__ void produce(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                                        const Range& range, const Start& st, const Ring& ring, int32_t who) {
+    const int lane = threadIdx.x & 31;
+    const int32_t P = p.c.page_size;
+    Cursor<S::ROWS> c;
+    int32_t off = c.open(p, st);
+    IssuedLoads loads;
+    int32_t stage = who, phase = 0;
+    bool ok = true;
+    int32_t mine = who;                                    // this warp's next tile of the range
+    for (int32_t n = 0; n < range.n && ok;) {
+        const int32_t count = min(c.tiles - off, range.n - n);
+        while (mine < n + count && ok) {
+            // lane i looks up the page and the scales of tile mine + i PRODUCERS
+            const int32_t k = off + (mine - n) + lane * S::PRODUCERS;
+            int32_t row[2] = {-1, -1};
+            StageInfo si;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            const int64_t at = __shfl_sync(0xffffffffu, place, ((it - pages_at) << 1) + g);
+            for (int g = 0; g < 2; ++g) {
+                si.ks[g] = si.iv[g] = 1.0f;
+                si.lv[g] = P_SHIFT;
+                si.valid[g] = 0;
+                const int32_t tok = k * A_TOK + 16 * g;
+                if (k >= off + count || tok >= c.sees) continue;
+                const int32_t page = __ldg(p.c.table + (int64_t)c.b * p.c.table_stride + tok / P);
+                if (page < 0 || page >= p.c.num_pages) {
+                    report_status(p.c.status, FP8_ERR_INVALID_ARG);
+                    continue;
+                }
+                const int64_t at = (int64_t)page * p.c.kv_heads + c.h;
+                row[g] = (int32_t)(at * P + tok % P);
+                si.ks[g] = __ldg(p.c.k_scale + at);
+                const float vs = __ldg(p.c.v_scale + at);
+                si.lv[g] = __log2f(vs) + P_SHIFT;
+                si.iv[g] = __frcp_rn(vs);
+                si.valid[g] = min(16, c.sees - tok);
+            }
+            for (int32_t j = 0; j < 32 && mine < n + count; ++j, mine += S::PRODUCERS) {
+                if (ok) ok = wait_bounded(&ring.empty[stage], (phase & 1) ^ 1, ring.abort_flag, p.c.status, p.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == j) ring.info[stage] = si;
+                const int32_t row0 = __shfl_sync(0xffffffffu, row[0], j), row1 = __shfl_sync(0xffffffffu, row[1], j);
+                __syncwarp();
+                if (lane == 0) {
+                    uint8_t* dst = ring.data + stage * S::STAGE;
+                    // a copy of 32 rows covers both halves (they are in one page)
+                    const int32_t copies = p.box == A_TOK ? (row0 >= 0 ? 1 : 0) : (row0 >= 0) + (row1 >= 0);
+                    ptx::mbar_arrive_expect_tx(&ring.full[stage], (uint32_t)(2 * copies * p.box * D));
+                    if (row0 >= 0) {
+                        ptx::tma_load_2d(dst, &tk, &ring.full[stage], 0, row0);
+                        ptx::tma_load_2d(dst + A_TOK * D, &tv, &ring.full[stage], 0, row0);
+                    }
+                    if (row1 >= 0 && p.box != A_TOK) {
+                        ptx::tma_load_2d(dst + 16 * D, &tk, &ring.full[stage], 0, row1);
+                        ptx::tma_load_2d(dst + (A_TOK + 16) * D, &tv, &ring.full[stage], 0, row1);
+                    }
+                }
+                loads.note((uint32_t)stage, (uint32_t)phase);
+                __syncwarp();
+                stage += S::PRODUCERS;
+                if (stage >= S::STAGES) stage -= S::STAGES, ++phase;
+            }
+        }
+        n += count;
+        off = 0;
+        if (n < range.n) c.next(p);
+    }
+    __syncwarp();
+    if (lane == 0) loads.drain(ring.full, p.c.status);     // every copy has landed before the CTA may exit
+}
+
+// ---------------------------------------------------------------- the consumers
+// Fragment layouts (c = lane % 4, r = lane / 4; mma m16n8k16).  The cached tokens (for the scores)
+// and the head's elements (for the output) are the instruction's 16 rows, the queries its 8
+// columns: grouped heads of 8 rows then waste no half of an instruction.
+//   scores[token, q] = K Q^T: the reduction index is permuted so that a lane's operands are 16
+//     contiguous bytes of a token's K row (chunk 2c + h at D = 128, c at 64: each phase of
+//     eight lanes then reads all banks once).
+//   out[d, q] += V^T W: m-tile j holds d = (D / 8) row + 2j, + 1 (rows r, r + 8), so that a lane's
+//     operands are D / 8 contiguous bytes of a V row.  W [token, q] leaves the scores'
+//     accumulator layout through an 8 x 8 transposition.
+template <int FMT, int D, int NQ>
+struct Consumer {
+    static constexpr int KK = D / 16;          // k-steps of the scores
+    static constexpr int MT = D / 16;          // m-tiles of the output
+    static constexpr int CH = D / 64;          // 16-byte chunks of a K row per lane
+    uint32_t qb[NQ][KK][2];
+    float qf[NQ][2];                           // of queries 8 nq + 2c, + 1
+    int32_t limit[NQ][2];                      // tokens the query sees (0: no such row)
+    int32_t least;                             // tokens the tile's first row sees
+    float o[NQ][MT][4], m[NQ][2], l[NQ][2];
+
+    __device__ __forceinline__ void open(const AttnParams& p, const Cursor<8 * NQ>& u) {
+        const int lane = threadIdx.x & 31, c = lane & 3, r = lane >> 2;
+        const int32_t rows = u.s.n * p.group, row0 = u.rt * 8 * NQ;
+        least = max(0, u.s.kv_len - u.s.n + row0 / p.group + 1);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < NQ; ++i) {
+            const int32_t row = row0 + r + 8 * i;
+            const bool real = row < rows;
+            const int32_t tok = real ? row / p.group : 0;
+            const uint16_t* src = p.q + (int64_t)(u.s.first + tok) * p.ldq +
+                                  (int64_t)(u.h * p.group + (real ? row % p.group : 0)) * D + 16 * CH * c;
+            uint4 v[CH][2];
+            uint32_t m2 = 0;
 #pragma unroll
-                for (int h = 0; h < CH; ++h) {
-                    kb[2 * g + i][h] = make_uint4(0, 0, 0, 0);
-                    if (at >= 0) kb[2 * g + i][h] = ld_v4_stream(p.c.k + at + (8 * i + r) * D + h * 64 + 16 * c);
+            for (int h = 0; h < CH; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    v[h][e] = real ? ld_v4(src + 16 * h + 8 * e) : make_uint4(0, 0, 0, 0);
+                    m2 = max_bf16x2_bits(m2, max_bf16x2_bits(max_bf16x2_bits(abs_bf16x2(v[h][e].x), abs_bf16x2(v[h][e].y)),
+                                                             max_bf16x2_bits(abs_bf16x2(v[h][e].z), abs_bf16x2(v[h][e].w))));
+                }
+            uint32_t top = hmax_pair(m2);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = max(1, min((int)(top >> 7), 253));                // biased exponent of the row's largest
+            const float inv = __uint_as_float((uint32_t)(254 - e) << 23);   // 2^(127 - e)
+            const float f = __uint_as_float((uint32_t)e << 23) * p.scale2;
+            const int32_t lim = real ? max(0, u.s.kv_len - u.s.n + tok + 1) : 0;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                qf[i][x] = __shfl_sync(0xffffffffu, f, 4 * (2 * c + x));
+                limit[i][x] = __shfl_sync(0xffffffffu, lim, 4 * (2 * c + x));
+                m[i][x] = -INFINITY;
+                l[i][x] = 0.0f;
+            }
+#pragma unroll
+            for (int h = 0; h < CH; ++h)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t w0 = k < 2 ? (k == 0 ? v[h][0].x : v[h][0].z) : (k == 2 ? v[h][1].x : v[h][1].z);
+                    const uint32_t w1 = k < 2 ? (k == 0 ? v[h][0].y : v[h][0].w) : (k == 2 ? v[h][1].y : v[h][1].w);
+                    qb[i][4 * h + k][0] = pack_half2(bf16_lo(w0) * inv, bf16_hi(w0) * inv);
+                    qb[i][4 * h + k][1] = pack_half2(bf16_lo(w1) * inv, bf16_hi(w1) * inv);
+                }
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[i][j][x] = 0.0f;
+        }
+    }
+
+    // One work tile: tokens tok0 .. tok0 + 31 in `st`.
+    __device__ __forceinline__ void tile(const uint8_t* st, const StageInfo& si, int32_t tok0) {
+        const int lane = threadIdx.x & 31, c = lane & 3, r = lane >> 2;
+        // s[i][g][x + 2y]: token 16 g + r + 8 y, query 8 i + 2c + x
+        float s[NQ][2][4];
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) s[i][g][x] = 0.0f;
+#pragma unroll
+        for (int h = 0; h < CH; ++h) {
+            uint4 v[2][2];
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                    v[g][y] = *reinterpret_cast<const uint4*>(st + stage_chunk<D>(16 * g + 8 * y + r, CH * c + h));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const uint32_t w0 = k == 0 ? v[g][0].x : k == 1 ? v[g][0].y : k == 2 ? v[g][0].z : v[g][0].w;
+                    const uint32_t w1 = k == 0 ? v[g][1].x : k == 1 ? v[g][1].y : k == 2 ? v[g][1].z : v[g][1].w;
+                    uint32_t a[4];
+                    half2x2_of<FMT>(w0, a[0], a[2]);
+                    half2x2_of<FMT>(w1, a[1], a[3]);
+#pragma unroll
+                    for (int i = 0; i < NQ; ++i) mma16816(s[i][g], a, qb[i][4 * h + k][0], qb[i][4 * h + k][1]);
                 }
         }
-    };
-    auto load_v = [&](int32_t it) {
+        const float4 f0 = *reinterpret_cast<const float4*>(&si);        // ks[2], lv[2]
+        const int4 f1 = *(reinterpret_cast<const int4*>(&si) + 1);      // iv[2], valid[2]
+        const float ks[2] = {f0.x, f0.y}, lv[2] = {f0.z, f0.w};
+        const float iv[2] = {__int_as_float(f1.x), __int_as_float(f1.y)};
+        const int32_t valid[2] = {f1.z, f1.w};
+        const bool edge = tok0 + A_TOK > least || valid[0] < 16 || valid[1] < 16;
+        bool move = false;
+        float top[NQ][2];
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const float f = qf[i][x] * ks[g];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) s[i][g][x + 2 * y] = fmaf(s[i][g][x + 2 * y], f, lv[g]);
+                }
+            }
+        if (edge) {
+#pragma unroll
+            for (int i = 0; i < NQ; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int g = 0; g < 2; ++g)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            if (tok0 + 16 * g + r + 8 * y >= limit[i][x] || r + 8 * y >= valid[g])
+                                s[i][g][x + 2 * y] = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                top[i][x] = fmaxf(fmaxf(s[i][0][x], s[i][0][x + 2]), fmaxf(s[i][1][x], s[i][1][x + 2])) - P_SHIFT;
+                move |= top[i][x] > m[i][x] + P_LAG;
+            }
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int i = 0; i < NQ; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float t = top[i][x];
+#pragma unroll
+                    for (int b = 4; b < 32; b <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, b));
+                    t = fmaxf(t, m[i][x]);
+                    const float corr = t == -INFINITY ? 1.0f : ex2(m[i][x] - t);
+                    m[i][x] = t;
+                    l[i][x] *= corr;
+#pragma unroll
+                    for (int j = 0; j < MT; ++j) {
+                        o[i][j][x] *= corr;
+                        o[i][j][x + 2] *= corr;
+                    }
+                }
+        }
+        uint32_t wb[NQ][2][2];                   // W as the B operand: [query][16 tokens][8 of them]
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float base = m[i][x] == -INFINITY ? 0.0f : m[i][x];
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) s[i][g][x + 2 * y] = ex2(s[i][g][x + 2 * y] - base);
+                    l[i][x] = fmaf(s[i][g][x] + s[i][g][x + 2], iv[g], l[i][x]);
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                    wb[i][g][y] = transpose8x8(pack_half2(s[i][g][2 * y], s[i][g][2 * y + 1]));
+        }
+        const uint8_t* sv = st + A_TOK * D;
+        constexpr int NW = D / 32;               // words of V per lane and token
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            const int64_t at = __shfl_sync(0xffffffffu, place, ((it - pages_at) << 1) + g);
-            const int32_t left = end - (begin + it * A_CTA_STEP + warp * A_STEP + 16 * g);   // tokens of the group
+            uint32_t w[4][NW];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int tok = 2 * c + (i & 1) + 8 * (i >> 1);
-                // slots past the last token may hold anything: they count as zeros
-                const bool in = at >= 0 && tok < left;
-                const uint8_t* src = p.c.v + (in ? at : 0) + tok * D + r * NT;
-                if (NT == 16) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (in) v = ld_v4_stream(src);
-                    vb[4 * g + i][0] = make_uint2(v.x, v.y);
-                    vb[4 * g + i][NT / 8 - 1] = make_uint2(v.z, v.w);
+                if (D == 128) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(sv + stage_chunk<D>(16 * g + tok, r));
+                    w[i][0] = v.x; w[i][1] = v.y; w[i][NW - 2] = v.z; w[i][NW - 1] = v.w;
                 } else {
-                    vb[4 * g + i][0] = make_uint2(0, 0);
-                    if (in) vb[4 * g + i][0] = __ldcs(reinterpret_cast<const uint2*>(src));
+                    const uint2 v = *reinterpret_cast<const uint2*>(sv + stage_chunk<D>(16 * g + tok, r >> 1) + 8 * (r & 1));
+                    w[i][0] = v.x; w[i][1] = v.y;
+                }
+                // slots past the last token may hold anything: they count as zeros
+                if (edge && tok >= valid[g]) {
+#pragma unroll
+                    for (int q = 0; q < NW; ++q) w[i][q] = 0;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < NW; ++q) {
+                uint32_t a0[4], a1[4];           // m-tiles 2q and 2q + 1: d = .. + 4q, 4q + 1 and 4q + 2, 4q + 3
+                half2x2_of<FMT>(__byte_perm(w[0][q], w[1][q], 0x5140), a0[0], a0[1]);
+                half2x2_of<FMT>(__byte_perm(w[0][q], w[1][q], 0x7362), a1[0], a1[1]);
+                half2x2_of<FMT>(__byte_perm(w[2][q], w[3][q], 0x5140), a0[2], a0[3]);
+                half2x2_of<FMT>(__byte_perm(w[2][q], w[3][q], 0x7362), a1[2], a1[3]);
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+                    mma16816(o[i][2 * q], a0, wb[i][g][0], wb[i][g][1]);
+                    mma16816(o[i][2 * q + 1], a1, wb[i][g][0], wb[i][g][1]);
                 }
             }
         }
-    };
-    if (iters > 0) {
-        hold(0);
-        load_k(0);
-        load_v(0);
     }
-    for (int32_t it = 0; it < iters; ++it) {
-        const int32_t tok0 = begin + it * A_CTA_STEP + warp * A_STEP;
-        const float ks[2] = {__shfl_sync(0xffffffffu, ksc, ((it - pages_at) << 1)),
-                             __shfl_sync(0xffffffffu, ksc, ((it - pages_at) << 1) + 1)};
-        const float vs[2] = {__shfl_sync(0xffffffffu, vsc, ((it - pages_at) << 1)),
-                             __shfl_sync(0xffffffffu, vsc, ((it - pages_at) << 1) + 1)};
-        const int64_t pl[2] = {__shfl_sync(0xffffffffu, place, ((it - pages_at) << 1)),
-                               __shfl_sync(0xffffffffu, place, ((it - pages_at) << 1) + 1)};
-        // ---- scores
-        float s[4][4];
+
+    // This warp's part of a unit, into shared memory.
+    template <class S>
+    __device__ __forceinline__ void put(float* part /* [ROWS][LD] */, float2* ml /* [ROWS] */) {
+        const int lane = threadIdx.x & 31, c = lane & 3, r = lane >> 2;
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
+        for (int i = 0; i < NQ; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
+            for (int x = 0; x < 2; ++x) {
 #pragma unroll
-            for (int h = 0; h < CH; ++h) {
-                const uint32_t w[4] = {kb[n][h].x, kb[n][h].y, kb[n][h].z, kb[n][h].w};
+                for (int b = 4; b < 32; b <<= 1) l[i][x] += __shfl_xor_sync(0xffffffffu, l[i][x], b);
+                const int row = 8 * i + 2 * c + x;
+                if (r == 0) ml[row] = make_float2(m[i][x], l[i][x]);
+                float4* dst = reinterpret_cast<float4*>(part + row * S::LD + (D / 8) * r);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma16816(s[n], qa[4 * h + k], half2_of<FMT>(w[k]), half2_of<FMT>(w[k] >> 16));
+                for (int j = 0; j < MT; j += 2)
+                    dst[j / 2] = make_float4(o[i][j][x], o[i][j][x + 2], o[i][j + 1][x], o[i][j + 1][x + 2]);
             }
-        }
-        if (it + 1 < iters) {
-            hold(it + 1);
-            load_k(it + 1);
-        }
-        // ---- weights
-        float lv[2], iv[2];
+    }
+};
+
+__device__ __forceinline__ uint16_t* out_row(const AttnParams& p, const Sequence& s, int32_t h, int32_t row, int32_t D) {
+    return p.out + (int64_t)(s.first + row / p.group) * p.ldo + (int64_t)(h * p.group + row % p.group) * D;
+}
+
+// The joining warp: sums the consumers' parts of each unit, and writes the output (a unit whose
+// tiles are all in this range) or the CTA's part of it.
+template <int D, class S>
+__device__ __forceinline__ void join_parts(const AttnParams& p, const Range& range, const Start& st, const float* part,
+                                           const float2* ml, uint64_t* jfull, uint64_t* jfree,
+                                           volatile int32_t* abort_flag) {
+    const int lane = threadIdx.x & 31;
+    Cursor<S::ROWS> u;
+    int32_t off = u.open(p, st);
+    uint32_t seg = 0;
+    int4 goes_on = make_int4(-1, 0, 0, 0);
+    for (int32_t n = 0; n < range.n; ++seg) {
+        const int32_t count = min(u.tiles - off, range.n - n);
+        bool ok = wait_bounded(jfull, seg & 1u, abort_flag, p.c.status, p.wait_ns);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const bool whole = count == u.tiles;
+        const int32_t slot = 2 * (int32_t)blockIdx.x + (n == 0 ? 0 : 1);
+        const int32_t rows = min(S::ROWS, u.s.n * p.group - u.rt * S::ROWS);
+        for (int32_t row = 0; row < rows; ++row) {
+            // lanes hold the warps' maxima and sums
+            const float2 a = lane < S::WARPS ? ml[lane * S::ROWS + row] : make_float2(-INFINITY, 0.0f);
+            float top = a.x;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            lv[g] = __log2f(vs[g]) + P_SHIFT;
-            iv[g] = __frcp_rn(vs[g]);
-        }
-        const bool edge = tok0 + A_STEP > least || pl[0] < 0 || pl[1] < 0;
+            for (int b = 16; b > 0; b >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, b));
+            const float f = top == -INFINITY ? 0.0f : ex2(a.x - top);
+            float l = a.y * f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float top = -INFINITY;
+            for (int b = 16; b > 0; b >>= 1) l += __shfl_xor_sync(0xffffffffu, l, b);
+            constexpr int V = D / 32;
+            float v[V];
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const float f = qf[i] * ks[n >> 1];
+            for (int e = 0; e < V; ++e) v[e] = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float z = fmaf(s[n][2 * i + e], f, lv[n >> 1]);
-                    if (edge && (tok0 + 8 * n + 2 * c + e >= min(limit[i], end) || pl[n >> 1] < 0)) z = -INFINITY;
-                    s[n][2 * i + e] = z;
-                    top = fmaxf(top, z);
+            for (int w = 0; w < S::WARPS; ++w) {
+                const float g = __shfl_sync(0xffffffffu, f, w);
+                const float* src = part + (w * S::ROWS + row) * S::LD + V * lane;
+                if (V == 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(src);
+                    v[0] = fmaf(x.x, g, v[0]); v[1] = fmaf(x.y, g, v[1]);
+                    v[V - 2] = fmaf(x.z, g, v[V - 2]); v[V - 1] = fmaf(x.w, g, v[V - 1]);
+                } else {
+                    const float2 x = *reinterpret_cast<const float2*>(src);
+                    v[0] = fmaf(x.x, g, v[0]); v[1] = fmaf(x.y, g, v[1]);
                 }
             }
-            top = quad_max(top);
-            const float m_new = fmaxf(mrow[i], top - P_SHIFT);
-            const float base = m_new == -INFINITY ? 0.0f : m_new;
-            const float corr = ex2(mrow[i] - base);
-            mrow[i] = m_new;
-            float sum = 0.0f;
+            if (whole) {
+                const float inv = l > 0.0f ? __frcp_rn(l) : 0.0f;
+                uint32_t* dst = reinterpret_cast<uint32_t*>(out_row(p, u.s, u.h, u.rt * S::ROWS + row, D)) + V / 2 * lane;
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                float part = 0.0f;
+                for (int e = 0; e < V / 2; ++e) dst[e] = pack_bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv);
+            } else {
+                float* dst = p.part_o + ((int64_t)slot * 16 + row) * D + V * lane;
 #pragma unroll
-                for (int n = 2 * g; n < 2 * g + 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float w = ex2(s[n][2 * i + e] - base);
-                        s[n][2 * i + e] = w;
-                        part += w;
-                    }
-                sum = fmaf(part, iv[g], sum);
-            }
-            lrow[i] = fmaf(lrow[i], corr, sum);
-            if (__any_sync(0xffffffffu, corr != 1.0f)) {
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    o[j][2 * i] *= corr;
-                    o[j][2 * i + 1] *= corr;
-                }
+                for (int e = 0; e < V; ++e) dst[e] = v[e];
+                if (lane == 0) p.part_ml[(int64_t)slot * 16 + row] = make_float2(top, l);
             }
         }
-        // ---- the values
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            const uint32_t a[4] = {pack_half2(s[2 * g][0], s[2 * g][1]), pack_half2(s[2 * g][2], s[2 * g][3]),
-                                   pack_half2(s[2 * g + 1][0], s[2 * g + 1][1]),
-                                   pack_half2(s[2 * g + 1][2], s[2 * g + 1][3])};
-#pragma unroll
-            for (int q = 0; q < NT / 4; ++q) {
-                uint32_t w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = (q & 1) ? vb[4 * g + i][q >> 1].y : vb[4 * g + i][q >> 1].x;
-                const uint32_t lo0 = __byte_perm(w[0], w[1], 0x5140), hi0 = __byte_perm(w[0], w[1], 0x7362);
-                const uint32_t lo1 = __byte_perm(w[2], w[3], 0x5140), hi1 = __byte_perm(w[2], w[3], 0x7362);
-                mma16816(o[4 * q + 0], a, half2_of<FMT>(lo0), half2_of<FMT>(lo1));
-                mma16816(o[4 * q + 1], a, half2_of<FMT>(lo0 >> 16), half2_of<FMT>(lo1 >> 16));
-                mma16816(o[4 * q + 2], a, half2_of<FMT>(hi0), half2_of<FMT>(hi1));
-                mma16816(o[4 * q + 3], a, half2_of<FMT>(hi0 >> 16), half2_of<FMT>(hi1 >> 16));
-            }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(jfree);
+        n += count;
+        if (n >= range.n && !whole && off == 0) {          // begins here, ends in a later CTA
+            const int64_t last = range.lo + n - count + u.tiles - 1;
+            int32_t i = (int32_t)(last * range.ctas / range.total);
+            while (range_begin(range.total, range.ctas, i + 1) <= last) ++i;
+            while (range_begin(range.total, range.ctas, i) > last) --i;
+            goes_on = make_int4(u.b, u.h * p.row_tiles + u.rt, slot, i);
         }
-        if (it + 1 < iters) load_v(it + 1);
+        off = 0;
+        if (n < range.n) u.next(p);
     }
-    // ---- join the warps
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        lrow[i] = quad_sum(lrow[i]);
-        if (c == 0) sml[warp][r + 8 * i] = make_float2(mrow[i], lrow[i]);
-    }
-    __syncthreads();
-    float keep[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        float m = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < A_WARPS; ++w) m = fmaxf(m, sml[w][r + 8 * i].x);
-        keep[i] = m == -INFINITY ? 0.0f : ex2(mrow[i] - m);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int j = 0; j < NT; j += 4)
-            *reinterpret_cast<float4*>(&so[warp][r + 8 * (e >> 1)][NT * (2 * c + (e & 1)) + j]) =
-                make_float4(o[j][e] * keep[e >> 1], o[j + 1][e] * keep[e >> 1], o[j + 2][e] * keep[e >> 1],
-                            o[j + 3][e] * keep[e >> 1]);
-    __syncthreads();
-    for (int32_t k = threadIdx.x; k < A_ROWS * D / 8; k += A_THREADS) {
-        const int32_t row = k / (D / 8), d = (k % (D / 8)) * 8;
-        if (t.row0 + row >= t.rows) continue;
-        float m = -INFINITY, l = 0.0f;
-#pragma unroll
-        for (int w = 0; w < A_WARPS; ++w) m = fmaxf(m, sml[w][row].x);
-#pragma unroll
-        for (int w = 0; w < A_WARPS; ++w)
-            if (m != -INFINITY) l = fmaf(sml[w][row].y, ex2(sml[w][row].x - m), l);
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            v[e] = 0.0f;
-#pragma unroll
-            for (int w = 0; w < A_WARPS; ++w) v[e] += so[w][row][d + e];
+    if (lane == 0) p.joins[blockIdx.x] = goes_on;
+}
+
+template <int FMT, int D, int NQ>
+__global__ void __launch_bounds__(Shape<D, NQ>::THREADS, 1)
+kv_attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                    const __grid_constant__ AttnParams p) {
+    using S = Shape<D, NQ>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Ring ring;
+    ring.full = reinterpret_cast<uint64_t*>(smem);
+    ring.empty = ring.full + A_MAX_STAGES;
+    uint64_t* jfull = ring.empty + A_MAX_STAGES;
+    uint64_t* jfree = jfull + 1;
+    ring.abort_flag = reinterpret_cast<volatile int32_t*>(jfree + 1);
+    Start* start = reinterpret_cast<Start*>(smem + 512);
+    int64_t* sums = reinterpret_cast<int64_t*>(smem + 640);
+    ring.data = smem + A_HEADER;
+    float* part = reinterpret_cast<float*>(ring.data + S::STAGES * S::STAGE);
+    float2* ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(part) + S::PART_BYTES);
+    ring.info = reinterpret_cast<StageInfo*>(reinterpret_cast<uint8_t*>(ml) + S::ML_BYTES);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_launch_dependents();                  // the joining kernel waits for this grid itself
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::STAGES; ++i) {
+            ptx::mbar_init(&ring.full[i], 1);
+            ptx::mbar_init(&ring.empty[i], 1);
         }
-        if (used == 1) {
-            const float inv = l > 0.0f ? __frcp_rn(l) : 0.0f;
-            uint16_t* dst = p.out + (int64_t)(t.s.first + (t.row0 + row) / p.group) * p.ldo +
-                            (int64_t)(t.head * p.group + (t.row0 + row) % p.group) * D + d;
-            *reinterpret_cast<uint4*>(dst) =
-                make_uint4(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv),
-                           pack_bf16x2(v[4] * inv, v[5] * inv), pack_bf16x2(v[6] * inv, v[7] * inv));
-        } else {
-            const int64_t at = ((int64_t)unit * p.splits + split) * A_ROWS + row;
-            float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + d);
-            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-            if (d == 0) p.part_ml[at] = make_float2(m, l);
+        ptx::mbar_init(jfull, S::WARPS);
+        ptx::mbar_init(jfree, 1);
+        *ring.abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&tk);
+        ptx::prefetch_tmap(&tv);
+    }
+    const Range range = find_range<S>(p, start, sums);       // syncs
+    if (range.n == 0) {
+        if (threadIdx.x == 0) p.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        return;
+    }
+    if (warp >= S::WARPS) {
+        if (warp == S::WARPS + S::PRODUCERS)
+            join_parts<D, S>(p, range, *start, part, ml, jfull, jfree, ring.abort_flag);
+        else
+            produce<D, S>(p, tk, tv, range, *start, ring, warp - S::WARPS);
+        return;
+    }
+    Cursor<S::ROWS> u;
+    int32_t off = u.open(p, *start);
+    Consumer<FMT, D, NQ> w;
+    int32_t mine = warp;                      // this warp's next tile of the range
+    int32_t stage = warp, phase = 0;
+    while (stage >= S::STAGES) stage -= S::STAGES, ++phase;
+    uint32_t seg = 0;
+    bool ok = true;
+    for (int32_t n = 0; n < range.n && ok; ++seg) {
+        const int32_t count = min(u.tiles - off, range.n - n);
+        w.open(p, u);
+        while (mine < n + count) {
+            // the lanes agree on a wait's outcome: the tile's shuffles need all of them
+            ok = wait_bounded(&ring.full[stage], phase & 1, ring.abort_flag, p.c.status, p.wait_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            w.tile(ring.data + stage * S::STAGE, ring.info[stage], (off + mine - n) * A_TOK);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&ring.empty[stage]);
+            mine += S::WARPS;
+            stage += S::WARPS;
+            while (stage >= S::STAGES) stage -= S::STAGES, ++phase;
         }
+        // the parts' buffer is free once the unit before has been joined
+        if (ok && seg > 0) ok = wait_bounded(jfree, (seg - 1) & 1u, ring.abort_flag, p.c.status, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        w.template put<S>(part + warp * S::ROWS * S::LD, ml + warp * S::ROWS);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(jfull);
+        n += count;
+        off = 0;
+        if (n < range.n) u.next(p);
     }
 }
 
 // ---------------------------------------------------------------- the joining kernel
-// One thread per 8 elements of a row; nothing to do for rows that one split covered.
+// A unit that several CTAs shared: its parts are slot j.z of the CTA where it begins and slot 0
+// of each CTA up to the last.  A CTA joins 4 rows: 4 groups of threads take every fourth part.
+constexpr int J_ROWS = 4, J_GROUPS = 4;
+
 template <int D>
-__global__ void __launch_bounds__(A_ROWS * D / 8) kv_attention_join_kernel(const __grid_constant__ AttnParams p) {
-    const int32_t unit = (int32_t)blockIdx.x;
-    const Tile t = tile_of(p, unit);
-    if (!t.s.ok || t.row0 >= t.rows) return;
-    const int32_t used = (t.see + p.chunk - 1) / p.chunk;
-    if (used <= 1) return;
-    const int32_t row = threadIdx.x / (D / 8), d = (threadIdx.x % (D / 8)) * 8;
-    if (t.row0 + row >= t.rows) return;
-    const int64_t at = (int64_t)unit * p.splits * A_ROWS + row;
-    float m = -INFINITY;
-    for (int32_t s = 0; s < used; ++s) m = fmaxf(m, p.part_ml[at + (int64_t)s * A_ROWS].x);
+__global__ void __launch_bounds__(J_ROWS * J_GROUPS * D / 8)
+kv_attention_join_kernel(const __grid_constant__ AttnParams p, int32_t tile_rows) {
+    __shared__ float so[J_GROUPS][J_ROWS][D];
+    __shared__ float sl[J_GROUPS][J_ROWS];
+    pdl_wait();
+    const int4 j = p.joins[blockIdx.x];
+    if (j.x < 0) return;
+    const Sequence s = sequence_of(p.c, j.x, p.max_kv);
+    const int32_t h = j.y / p.row_tiles, rt = j.y % p.row_tiles;
+    const int32_t parts = j.w - (int32_t)blockIdx.x + 1;
+    constexpr int VEC = D / 8;
+    const int32_t d = (threadIdx.x % VEC) * 8, lrow = (threadIdx.x / VEC) % J_ROWS, grp = threadIdx.x / (VEC * J_ROWS);
+    const int32_t row = blockIdx.y * J_ROWS + lrow;
+    const bool real = rt * tile_rows + row < s.n * p.group;
+    auto slot = [&](int32_t i) { return (int64_t)(i == 0 ? j.z : 2 * ((int32_t)blockIdx.x + i)) * 16 + row; };
     float l = 0.0f, v[8] = {};
-    if (m != -INFINITY) {
-        for (int32_t s = 0; s < used; ++s) {
-            const float2 ml = p.part_ml[at + (int64_t)s * A_ROWS];
-            const float f = ex2(ml.x - m);
-            l = fmaf(ml.y, f, l);
-            const float4* src = reinterpret_cast<const float4*>(p.part_o + (at + (int64_t)s * A_ROWS) * D + d);
-            const float4 a = src[0], b = src[1];
-            v[0] = fmaf(a.x, f, v[0]); v[1] = fmaf(a.y, f, v[1]); v[2] = fmaf(a.z, f, v[2]); v[3] = fmaf(a.w, f, v[3]);
-            v[4] = fmaf(b.x, f, v[4]); v[5] = fmaf(b.y, f, v[5]); v[6] = fmaf(b.z, f, v[6]); v[7] = fmaf(b.w, f, v[7]);
+    if (real) {
+        float m = -INFINITY;
+        for (int32_t i = 0; i < parts; ++i) m = fmaxf(m, p.part_ml[slot(i)].x);
+        if (m != -INFINITY) {
+#pragma unroll 4
+            for (int32_t i = grp; i < parts; i += J_GROUPS) {
+                const int64_t at = slot(i);
+                const float2 ml = p.part_ml[at];
+                const float f = ex2(ml.x - m);
+                l = fmaf(ml.y, f, l);
+                const float4* src = reinterpret_cast<const float4*>(p.part_o + at * D + d);
+                const float4 a = src[0], b = src[1];
+                v[0] = fmaf(a.x, f, v[0]); v[1] = fmaf(a.y, f, v[1]); v[2] = fmaf(a.z, f, v[2]); v[3] = fmaf(a.w, f, v[3]);
+                v[4] = fmaf(b.x, f, v[4]); v[5] = fmaf(b.y, f, v[5]); v[6] = fmaf(b.z, f, v[6]); v[7] = fmaf(b.w, f, v[7]);
+            }
         }
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) so[grp][lrow][d + e] = v[e];
+    if (d == 0) sl[grp][lrow] = l;
+    __syncthreads();
+    if (grp != 0 || !real) return;
+    l = sl[0][lrow];
+#pragma unroll
+    for (int g = 1; g < J_GROUPS; ++g) {
+        l += sl[g][lrow];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += so[g][lrow][d + e];
+    }
     const float inv = l > 0.0f ? __frcp_rn(l) : 0.0f;
-    uint16_t* dst = p.out + (int64_t)(t.s.first + (t.row0 + row) / p.group) * p.ldo +
-                    (int64_t)(t.head * p.group + (t.row0 + row) % p.group) * D + d;
+    uint16_t* dst = out_row(p, s, h, rt * tile_rows + row, D) + d;
     *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv),
                                                 pack_bf16x2(v[4] * inv, v[5] * inv), pack_bf16x2(v[6] * inv, v[7] * inv));
 }
 
-// How the cached tokens are split: enough CTAs for about four waves of two per SM, and no
-// split shorter than 512 tokens (its partial result would cost more than it gives).
-struct Plan {
-    int64_t units;
-    int32_t row_tiles, splits, chunk;
-};
-Plan plan_of(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t max_q, int64_t max_kv) {
-    Plan pl;
-    const int64_t rows = (int64_t)max_q * (q_heads / kv_heads);
-    pl.row_tiles = (int32_t)((rows + A_ROWS - 1) / A_ROWS);
-    pl.units = (int64_t)batch * kv_heads * pl.row_tiles;
-    const int64_t want = std::max<int64_t>(1, 1184 / std::max<int64_t>(1, pl.units));
-    int64_t chunk = std::max<int64_t>(512, (max_kv + want - 1) / want);
-    chunk = (chunk + A_CTA_STEP - 1) / A_CTA_STEP * A_CTA_STEP;
-    pl.chunk = (int32_t)chunk;
-    pl.splits = (int32_t)std::max<int64_t>(1, (max_kv + chunk - 1) / chunk);
-    return pl;
+// ---------------------------------------------------------------- host side
+template <int FMT, int D, int NQ>
+cudaError_t launch_attention(AttnParams p, cudaStream_t st) {
+    using S = Shape<D, NQ>;
+    const int grid = num_sms();
+    p.row_tiles = (int32_t)(((int64_t)p.c.max_q * p.group + S::ROWS - 1) / S::ROWS);
+    const uint64_t rows = (uint64_t)p.c.num_pages * p.c.kv_heads * p.c.page_size;
+    if (rows >= ((uint64_t)1 << 31)) return cudaErrorInvalidValue;    // beyond any GPU's memory
+    p.box = std::min(p.c.page_size, A_TOK);
+    CUtensorMap tk, tv;
+    const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    memset(&tk, 0, sizeof(tk));
+    memset(&tv, 0, sizeof(tv));
+    if (rows > 0 && (!make_map_2d(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.c.k, D, rows, D, D, p.box, sw) ||
+                     !make_map_2d(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.c.v, D, rows, D, D, p.box, sw)))
+        return cudaErrorInvalidValue;
+    static bool attr_done[kDeviceCacheSlots];   // the attribute is set per device
+    const int ds = device_slot();
+    if (ds < 0 || !attr_done[ds]) {
+        const cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<FMT, D, NQ>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, A_SMEM);
+        if (e != cudaSuccess) return e;
+        if (ds >= 0) attr_done[ds] = true;
+    }
+    kv_attention_kernel<FMT, D, NQ><<<grid, S::THREADS, A_SMEM, st>>>(tk, tv, p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, S::ROWS / J_ROWS);
+    cfg.blockDim = dim3(J_ROWS * J_GROUPS * D / 8);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<D>, p, (int32_t)S::ROWS);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// 8 rows per tile where they hold all of a sequence's, 16 otherwise.
 template <int FMT, int D>
-cudaError_t launch_attention(const AttnParams& p, int64_t units, cudaStream_t st) {
-    kv_attention_kernel<FMT, D><<<(unsigned)(units * p.splits), A_THREADS, 0, st>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.splits == 1) return e;
-    kv_attention_join_kernel<D><<<(unsigned)units, A_ROWS * D / 8, 0, st>>>(p);
-    return cudaGetLastError();
+cudaError_t launch_rows(const AttnParams& p, cudaStream_t st) {
+    return (int64_t)p.c.max_q * p.group <= 8 ? launch_attention<FMT, D, 1>(p, st) : launch_attention<FMT, D, 2>(p, st);
+}
+
+// The workspace: [2 grid][16][D] floats, the joins, then [2 grid][16] pairs.
+size_t workspace_bytes(int32_t head_dim) {
+    return (size_t)num_sms() * (2 * 16 * (size_t)(head_dim + 2) * sizeof(float) + sizeof(int4));
 }
 
 }  // namespace
 
 size_t attention_workspace(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t max_q,
                            int64_t max_kv) {
-    const Plan pl = plan_of(batch, q_heads, kv_heads, max_q, max_kv);
-    if (pl.splits == 1) return 0;
-    return (size_t)pl.units * pl.splits * A_ROWS * (head_dim + 2) * sizeof(float);
+    (void)batch;
+    (void)q_heads;
+    (void)kv_heads;
+    (void)max_q;
+    (void)max_kv;
+    return workspace_bytes(head_dim);
 }
 
 cudaError_t launch_kv_attention(const AttnArgs& a, cudaStream_t st) {
-    const Plan pl = plan_of(a.c.batch, a.q_heads, a.c.kv_heads, a.c.max_q, a.max_kv);
-    if (pl.units * pl.splits >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
     AttnParams p{};
     p.c = a.c;
     p.q = a.q;
@@ -462,17 +849,15 @@ cudaError_t launch_kv_attention(const AttnArgs& a, cudaStream_t st) {
     p.max_kv = a.max_kv;
     p.q_heads = a.q_heads;
     p.group = a.q_heads / a.c.kv_heads;
-    p.row_tiles = pl.row_tiles;
-    p.splits = pl.splits;
-    p.chunk = pl.chunk;
     p.scale2 = a.softmax_scale * LOG2E;
+    p.wait_ns = wait_limit_ns();
+    const int64_t slots = 2 * (int64_t)num_sms();
     p.part_o = static_cast<float*>(a.workspace);
-    p.part_ml = reinterpret_cast<float2*>(p.part_o + pl.units * pl.splits * A_ROWS * a.c.head_dim);
+    p.joins = reinterpret_cast<int4*>(p.part_o + slots * 16 * a.c.head_dim);
+    p.part_ml = reinterpret_cast<float2*>(p.joins + slots / 2);
     if (a.c.fmt == FP8_E4M3)
-        return a.c.head_dim == 128 ? launch_attention<FP8_E4M3, 128>(p, pl.units, st)
-                                   : launch_attention<FP8_E4M3, 64>(p, pl.units, st);
-    return a.c.head_dim == 128 ? launch_attention<FP8_E5M2, 128>(p, pl.units, st)
-                               : launch_attention<FP8_E5M2, 64>(p, pl.units, st);
+        return a.c.head_dim == 128 ? launch_rows<FP8_E4M3, 128>(p, st) : launch_rows<FP8_E4M3, 64>(p, st);
+    return a.c.head_dim == 128 ? launch_rows<FP8_E5M2, 128>(p, st) : launch_rows<FP8_E5M2, 64>(p, st);
 }
 
 }  // namespace fp8b

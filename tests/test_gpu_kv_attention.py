@@ -135,6 +135,16 @@ def test_zero_queries_and_tokens_that_see_nothing():
     assert bool(torch.isfinite(out).all())
 
 
+def test_empty_caches():
+    p = Paged([0, 0], 2, 16, 64, 0, seed=11)
+    q = queries(p, 2, 4, 1)
+    for max_kv in (0, 64):
+        out, st = run(p, q, [1, 1], max_kv=max_kv)
+        assert st == 0 and bool((out == 0).all())
+    out, st = run(p, q, [0, 0])                     # no tokens in the call: nothing is written
+    assert st == 0 and bool(torch.isnan(out).all())
+
+
 def test_strided_rows_and_rows_behind_the_last_sequence():
     p = Paged([70, 33], 2, 32, 64, 0, seed=12)
     wide = queries(Paged([1], 12, 16, 64, 0), 10, 1, 2)             # 12 heads of 64 per row

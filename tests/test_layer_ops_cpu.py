@@ -120,7 +120,7 @@ def test_kv_attention_refusals():
     assert n > 0
     assert attend(max_kv=100000, ws=None) == b.FP8_ERR_WORKSPACE
     assert attend(max_kv=100000, ws_bytes=n - 1) == b.FP8_ERR_WORKSPACE
-    for bad in ((0, 4, 2, 64, 1, 10), (1, 4, 3, 64, 1, 10), (1, 4, 2, 96, 1, 10), (1, 4, 2, 64, 0, 10), (1, 4, 2, 64, 1, 0)):
+    for bad in ((0, 4, 2, 64, 1, 10), (1, 4, 3, 64, 1, 10), (1, 4, 2, 96, 1, 10), (1, 4, 2, 64, 0, 10), (1, 4, 2, 64, 1, -1)):
         assert b.fp8_kv_attention_workspace_size(*bad) == 0
 
 
