@@ -15,8 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp8.so")
 SOURCES = ["api.cu", "quantize.cu", "gemm_sm100.cu", "decode_sm100.cu", "wo_sm100.cu", "norm.cu", "kv_cache.cu",
-           "attention.cu", "noalloc.cu", "testing.cu"]
-HEADERS = ["common.cuh", "gemm_common.cuh", "kernels.h", "kv_common.cuh", "ptx.cuh"]
+           "attention.cu", "attention_prompt.cu", "noalloc.cu", "testing.cu"]
+HEADERS = ["attention_common.cuh", "common.cuh", "gemm_common.cuh", "kernels.h", "kv_common.cuh", "ptx.cuh"]
 PUBLIC_HEADERS = [os.path.join(os.path.dirname(HERE), "include", h) for h in ("fp8.h", "fp8_testing.h")]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

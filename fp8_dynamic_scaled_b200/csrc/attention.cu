@@ -15,8 +15,7 @@
 // the softmax is sum w / s_v.  M may lag behind the true maximum by 2^7, which fp16 has room
 // for: the sums are moved to a new M only when a score passes that, a rare event after the
 // first tiles.
-#include "gemm_common.cuh"
-#include "kv_common.cuh"
+#include "attention_common.cuh"
 
 namespace fp8b {
 
@@ -48,49 +47,11 @@ struct Shape {
     static_assert(TURN % WARPS == 0 && TURN % PRODUCERS == 0 && STAGES > 0, "stages have one owner on each side");
 };
 
-constexpr float LOG2E = 1.4426950408889634f;
-constexpr float P_SHIFT = 8.0f;        // the largest weight is 2^8 ..
-constexpr float P_LAG = 7.0f;          // .. to 2^15 (fp16 ends at 2^16)
-
-struct AttnParams {
-    KvArgs c;
-    const uint16_t* q;
-    uint16_t* out;
-    int64_t ldq, ldo, max_kv;
-    int32_t q_heads, group;
-    int32_t row_tiles;                // most row tiles of a (sequence, KV head)
-    int32_t box;                      // page rows of one copy: min(page_size, A_TOK)
-    float scale2;                     // softmax_scale * log2(e)
-    float* part_o;                    // [2 grid][16][D]: a CTA's first and last part of a unit
-    float2* part_ml;                  // [2 grid][16]: maximum (log2), sum
-    int4* joins;                      // [grid]: the unit that begins in CTA i and goes on in the next
-    uint64_t wait_ns;
-};
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// Four codes -> two pairs of fp16 values, exactly.
-template <int FMT>
-__device__ __forceinline__ void half2x2_of(uint32_t codes, uint32_t& lo, uint32_t& hi) {
-    if (FMT == FP8_E4M3)
-        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(codes));
-    else
-        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e5m2x2 %0, a;\n\t"
-            "cvt.rn.f16x2.e5m2x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(codes));
-}
-__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
 }
 // The 8 x 8 block of 16-bit values that a warp holds in fragment layout, transposed.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -561,10 +522,6 @@ struct Consumer {
     }
 };
 
-__device__ __forceinline__ uint16_t* out_row(const AttnParams& p, const Sequence& s, int32_t h, int32_t row, int32_t D) {
-    return p.out + (int64_t)(s.first + row / p.group) * p.ldo + (int64_t)(h * p.group + row % p.group) * D;
-}
-
 // The joining warp: sums the consumers' parts of each unit, and writes the output (a unit whose
 // tiles are all in this range) or the CTA's part of it.
 template <int D, class S>
@@ -816,10 +773,14 @@ cudaError_t launch_attention(AttnParams p, cudaStream_t st) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// 8 rows per tile where they hold all of a sequence's, 16 otherwise.
+// 8 rows per tile where they hold all of a sequence's, 16 up to a point, and from there the wide
+// tiles of the prompt kernel.
 template <int FMT, int D>
 cudaError_t launch_rows(const AttnParams& p, cudaStream_t st) {
-    return (int64_t)p.c.max_q * p.group <= 8 ? launch_attention<FMT, D, 1>(p, st) : launch_attention<FMT, D, 2>(p, st);
+    const int64_t rows = (int64_t)p.c.max_q * p.group;
+    if (rows <= 8) return launch_attention<FMT, D, 1>(p, st);
+    if (rows >= 64) return launch_prompt_attention(p, st);
+    return launch_attention<FMT, D, 2>(p, st);
 }
 
 // The workspace: [2 grid][16][D] floats, the joins, then [2 grid][16] pairs.

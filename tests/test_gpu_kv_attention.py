@@ -286,3 +286,11 @@ def test_weights_far_below_the_largest_still_count():
     assert st == 0
     assert math.exp(11.0) < n
     near(out, p, q, [1], scale=1.0)
+
+
+@pytest.mark.parametrize("group", [8, 16])
+def test_many_long_sequences(group):
+    """More sequences than a warp has lanes, and many tiles and several units per CTA (8 and 16 rows)."""
+    lens = [700 + 97 * (i % 13) for i in range(40)]
+    lens[3], lens[35] = 9001, 6400
+    check(Paged(lens, 4, 64, 128, 0, seed=19), [1] * 40, group)
