@@ -82,15 +82,15 @@ struct Codes {
     static constexpr int N = T_TOK / STEP;                      // chunks per thread
     uint4 v[N];
 
-    __device__ __forceinline__ void load(const uint8_t* base, const int64_t* place, int32_t t, int32_t left) {
+    // `place`: the offset of 16 tokens, -1 for none, in the lane first + their number in the step; rows at
+    // or past `left` are zeros (those slots may hold anything).
+    __device__ __forceinline__ void load(const uint8_t* base, int64_t place, int32_t first, int32_t t, int32_t left) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int32_t row = t / PER_ROW + STEP * i;
-            int64_t at = -1;
-            // the row's 16 tokens: their place is known to the lane of their number
-            at = __shfl_sync(0xffffffffu, *place, row >> 4);
+            const int64_t at = __shfl_sync(0xffffffffu, place, first + (row >> 4));
             v[i] = make_uint4(0, 0, 0, 0);
-            if (at >= 0 && row < left) v[i] = ld_v4(base + at + (int64_t)(row & 15) * D + (t % PER_ROW) * 16);
+            if (at >= 0 && row < left) v[i] = ld_v4(base + at + (row & 15) * D + (t % PER_ROW) * 16);
         }
     }
     __device__ __forceinline__ void store(uint8_t* tile, int32_t t) const {
@@ -118,47 +118,58 @@ __device__ __forceinline__ void convert(const AttnParams& p, const Unit& u, uint
     const int32_t t = threadIdx.x - 128, lane = t & 31;
     const int32_t P = p.c.page_size;
     const int32_t steps = max(u.steps[0], u.steps[1]);
-    int64_t place;
-    GroupInfo gi;
-    // lanes 0-7: the place and the scales of the 16 tokens of their number in step j
-    auto look = [&](int32_t j) {
+    // Lane i holds the place and the scales of 16 tokens of 4 steps: those of number i % 8 in step
+    // 4 B + i / 8 of batch B; the pages of the next batch are on the way meanwhile.
+    int32_t next_page = -1;
+    int64_t place = -1;
+    float ks = 0.0f, vs = 1.0f;
+    auto fetch = [&](int32_t batch) {
+        const int32_t tok = 16 * (32 * batch + lane);
+        next_page = -1;
+        if (tok < u.sees) next_page = __ldg(p.c.table + (int64_t)u.b * p.c.table_stride + tok / P);
+    };
+    auto take = [&](int32_t batch) {
+        const int32_t tok = 16 * (32 * batch + lane);
         place = -1;
-        gi.ks = 0.0f;
-        gi.lv = -INFINITY;
-        gi.iv = 1.0f;
-        gi.pad = 0.0f;
-        const int32_t tok = j * T_TOK + 16 * lane;
-        if (lane < T_GROUPS && tok < u.sees) {
-            const int32_t page = __ldg(p.c.table + (int64_t)u.b * p.c.table_stride + tok / P);
-            if (page >= 0 && page < p.c.num_pages) {
-                const int64_t at = (int64_t)page * p.c.kv_heads + u.h;
+        ks = 0.0f;
+        vs = 1.0f;
+        if (tok < u.sees) {
+            if (next_page >= 0 && next_page < p.c.num_pages) {
+                const int64_t at = (int64_t)next_page * p.c.kv_heads + u.h;
                 place = (at * P + tok % P) * D;
-                gi.ks = __ldg(p.c.k_scale + at);
-                const float vs = __ldg(p.c.v_scale + at);
-                gi.lv = __log2f(vs) + P_SHIFT;
-                gi.iv = __frcp_rn(vs);
+                ks = __ldg(p.c.k_scale + at);
+                vs = __ldg(p.c.v_scale + at);
             } else {
                 report_status(p.c.status, FP8_ERR_INVALID_ARG);
             }
         }
         __syncwarp();
+        fetch(batch + 1);
     };
     Codes<FMT, D> k, v;
-    look(0);
-    k.load(p.c.k, &place, t, u.sees);
+    fetch(0);
+    take(0);
+    k.load(p.c.k, place, 0, t, u.sees);
     for (int32_t j = 0; j < steps; ++j) {
-        const int32_t buf = j & 1;
+        const int32_t buf = j & 1, first = (j & 3) * T_GROUPS;
         const uint32_t parity = ((j >> 1) & 1) ^ 1;
-        v.load(p.c.v, &place, t, u.sees - j * T_TOK);
+        v.load(p.c.v, place, first, t, u.sees - j * T_TOK);
         if (!warp_wait(&bars->kempty[buf], parity, bars, p)) return;
         k.store(k16 + buf * tile_bytes<D>(), t);
-        if (t < T_GROUPS) info[j & 3][t] = gi;
+        if (t >= first && t < first + T_GROUPS) {          // warp 4's lanes of this step
+            GroupInfo gi;
+            gi.ks = ks;
+            gi.lv = place >= 0 ? __log2f(vs) + P_SHIFT : -INFINITY;
+            gi.iv = __frcp_rn(vs);
+            gi.pad = 0.0f;
+            info[j & 3][t - first] = gi;
+        }
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars->kfull[buf]);
         if (j + 1 < steps) {
-            look(j + 1);
-            k.load(p.c.k, &place, t, u.sees - (j + 1) * T_TOK);
+            if (((j + 1) & 3) == 0) take((j + 1) >> 2);
+            k.load(p.c.k, place, ((j + 1) & 3) * T_GROUPS, t, u.sees - (j + 1) * T_TOK);
         }
         if (!warp_wait(&bars->vempty[buf], parity, bars, p)) return;
         v.store(v16 + buf * tile_bytes<D>(), t);
@@ -234,6 +245,73 @@ __device__ __forceinline__ void issue(const AttnParams& p, const Unit& u, uint32
 }
 
 // ---------------------------------------------------------------- the rows
+// One step of a row: its 128 products s -> weights (fp16, over the products in tensor memory at
+// `ts`), the running maximum m (log2) and sum l; O at `to` follows a new maximum.  In units of
+// log2 a score is z = s f + a with f = qf s_k >= 0, a = log2 s_v per 16 tokens, so that a group's
+// largest score is that of its largest product.  EDGE: tokens at or past `left` are not seen.
+template <int D, bool EDGE>
+__device__ __forceinline__ void weights(const uint32_t (&s)[4][32], const GroupInfo* gi, int32_t left, float qf, float& m,
+                                        float& l, bool has_o, uint32_t ts, uint32_t to) {
+    float top = -INFINITY;                                 // with P_SHIFT in it
+#pragma unroll
+    for (int g = 0; g < T_GROUPS; ++g) {
+        float g0 = -INFINITY, g1 = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+            const float x = __uint_as_float(s[g >> 1][(g & 1) * 16 + e]);
+            const float y = __uint_as_float(s[g >> 1][(g & 1) * 16 + e + 1]);
+            if (!EDGE || 16 * g + e < left) g0 = fmaxf(g0, x);
+            if (!EDGE || 16 * g + e + 1 < left) g1 = fmaxf(g1, y);
+        }
+        g0 = fmaxf(g0, g1);
+        const float2 q = *reinterpret_cast<const float2*>(&gi[g]);
+        const float z = fmaf(g0, qf * q.x, q.y);
+        top = fmaxf(top, EDGE && g0 == -INFINITY ? -INFINITY : z);
+    }
+    const bool far = m == -INFINITY ? top > -INFINITY : top > m + (P_SHIFT + P_LAG);
+    if (__any_sync(0xffffffffu, far)) {
+        const float m_new = fmaxf(m, top - P_SHIFT);
+        const float corr = m_new == -INFINITY ? 1.0f : ex2(m - m_new);
+        m = m_new;
+        l *= corr;
+        if (has_o) {
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                ptx::tmem_ld_32x32b_x16(to + 16 * c, o);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                ptx::tmem_st_32x32b_x16(to + 16 * c, o);
+            }
+        }
+    }
+    const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int g = 2 * c + h;
+            const float4 q = *reinterpret_cast<const float4*>(&gi[g]);
+            const float2 f2 = make_float2(qf * q.x, qf * q.x), a2 = make_float2(q.y - base, q.y - base);
+            float2 part = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+                float2 z = fma2_rn(make_float2(__uint_as_float(s[c][16 * h + e]), __uint_as_float(s[c][16 * h + e + 1])),
+                                   f2, a2);
+                if (EDGE && 16 * g + e >= left) z.x = -INFINITY;
+                if (EDGE && 16 * g + e + 1 >= left) z.y = -INFINITY;
+                const float2 y = make_float2(ex2(z.x), ex2(z.y));
+                part = add2_rn(part, y);
+                w[8 * h + e / 2] = pack_half2(y.x, y.y);
+            }
+            l = fmaf(part.x + part.y, q.z, l);
+        }
+        ptx::tmem_st_32x32b_x16(ts + 16 * c, w);
+    }
+}
+
 // Warps 8-11 (i = 0) and 12-15 (i = 1): thread = row = TMEM lane.
 template <int D>
 __device__ __forceinline__ void rows(const AttnParams& p, const Unit& u, uint8_t* q16, const GroupInfo (*info)[T_GROUPS],
@@ -258,8 +336,9 @@ __device__ __forceinline__ void rows(const AttnParams& p, const Unit& u, uint8_t
                                                      max_bf16x2_bits(abs_bf16x2(v.z), abs_bf16x2(v.w))));
         }
         const int e = max(1, min((int)(hmax_pair(m2) >> 7), 253));
-        const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
-        qf = __uint_as_float((uint32_t)e << 23) * p.scale2;
+        // the sign of the softmax scale goes into Q, so that the largest product is the largest score
+        const float inv = copysignf(__uint_as_float((uint32_t)(254 - e) << 23), p.scale2);
+        qf = __uint_as_float((uint32_t)e << 23) * fabsf(p.scale2);
         for (int k = 0; k < D / 8; ++k) {
             const uint4 v = real ? ld_v4(src + 8 * k) : make_uint4(0, 0, 0, 0);
             *reinterpret_cast<uint4*>(q16 + i * tile_bytes<D>() + (k >> 3) * T_BLOCK + swizzled(trow, k & 7)) =
@@ -276,85 +355,16 @@ __device__ __forceinline__ void rows(const AttnParams& p, const Unit& u, uint8_t
     for (int32_t j = 0; j < u.steps[i]; ++j) {
         if (!warp_wait(&bars->sfull[i], j & 1, bars, p)) return;
         ptx::tc_fence_after();
-        // The scores are read from tensor memory twice, 32 at a time with the next 32 on the way: for
-        // their maximum, then for the weights.  (Holding all 128 in registers spills.)
-        const float base = m == -INFINITY ? 0.0f : m;
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x32(ts + 32 * c, s[c]);
+        ptx::tmem_ld_wait();
         const GroupInfo* gi = info[j & 3];
         const int32_t left = limit - j * T_TOK;
-        const bool edge = least - j * T_TOK < T_TOK;       // some row of the warp ends in this step
-        // scores 32 c .. in units of log2, + log2 s_v + P_SHIFT - sub
-        auto scaled = [&](const uint32_t (&x)[32], int c, float sub, float (&z)[32]) {
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const float4 q = *reinterpret_cast<const float4*>(&gi[2 * c + g]);
-                const float f = qf * q.x, a = q.y - sub;
-#pragma unroll
-                for (int e = 16 * g; e < 16 * g + 16; e += 2) {
-                    const float2 y = fma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
-                                             make_float2(f, f), make_float2(a, a));
-                    z[e] = y.x;
-                    z[e + 1] = y.y;
-                }
-            }
-            if (edge) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (32 * c + e >= left) z[e] = -INFINITY;
-            }
-        };
-        uint32_t x[2][32];
-        ptx::tmem_ld_32x32b_x32(ts, x[0]);
-        ptx::tmem_ld_wait();
-        float top2[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            ptx::tmem_ld_32x32b_x32(ts + 32 * ((c + 1) & 3), x[(c + 1) & 1]);     // the last: the first again
-            float z[32];
-            scaled(x[c & 1], c, base, z);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) top2[e & 1] = fmaxf(top2[e & 1], z[e]);
-            ptx::tmem_ld_wait();
-        }
-        const float top = fmaxf(top2[0], top2[1]);         // + base - P_SHIFT: the largest score
-        const bool far = m == -INFINITY ? top > -INFINITY : top > P_SHIFT + P_LAG;
-        if (__any_sync(0xffffffffu, far)) {
-            const float m_new = fmaxf(m, top - P_SHIFT + base);
-            const float corr = m_new == -INFINITY ? 1.0f : ex2(m - m_new);
-            m = m_new;
-            l *= corr;
-            if (j > 0) {
-#pragma unroll 1
-                for (int c = 0; c < D / 16; ++c) {
-                    uint32_t o[16];
-                    ptx::tmem_ld_32x32b_x16(to + 16 * c, o);
-                    ptx::tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-                    ptx::tmem_st_32x32b_x16(to + 16 * c, o);
-                }
-            }
-        }
-        const float sub = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            if (c < 3) ptx::tmem_ld_32x32b_x32(ts + 32 * (c + 1), x[(c + 1) & 1]);
-            float z[32];
-            scaled(x[c & 1], c, sub, z);
-            uint32_t w[16];
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                float2 part = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int e = 16 * g; e < 16 * g + 16; e += 2) {
-                    const float2 y = make_float2(ex2(z[e]), ex2(z[e + 1]));
-                    part = add2_rn(part, y);
-                    w[e / 2] = pack_half2(y.x, y.y);
-                }
-                l = fmaf(part.x + part.y, gi[2 * c + g].iv, l);
-            }
-            if (c < 3) ptx::tmem_ld_wait();
-            ptx::tmem_st_32x32b_x16(ts + 16 * c, w);       // over scores that have been read
-        }
+        if (least - j * T_TOK < T_TOK)                     // some row of the warp ends in this step
+            weights<D, true>(s, gi, left, qf, m, l, j > 0, ts, to);
+        else
+            weights<D, false>(s, gi, left, qf, m, l, j > 0, ts, to);
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         __syncwarp();
@@ -435,15 +445,15 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_prompt_attention_kernel(const
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bars->tmem_slot);
-    // registers: 128 a thread at launch, 512 for the four warpgroups together; 56 + 104 + 2 * 176 = 512
+    // registers: 128 a thread at launch, 512 for the four warpgroups together; 40 + 104 + 2 * 184 = 512
     if (warp < 4) {
-        ptx::regs_dec<56>();
+        ptx::regs_dec<40>();
         if (warp == 0) issue<D>(p, u, ptx::smem_u32(q16), ptx::smem_u32(k16), ptx::smem_u32(v16), tmem, bars);
     } else if (warp < 8) {
         ptx::regs_dec<104>();
         convert<FMT, D>(p, u, k16, v16, info, bars);
     } else {
-        ptx::regs_inc<176>();
+        ptx::regs_inc<184>();
         rows<D>(p, u, q16, info, tmem, bars);
     }
     ptx::tc_fence_before();
