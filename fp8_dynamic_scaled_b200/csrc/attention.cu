@@ -773,13 +773,25 @@ cudaError_t launch_attention(AttnParams p, cudaStream_t st) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// 8 rows per tile where they hold all of a sequence's, 16 up to a point, and from there the wide
-// tiles of the prompt kernel.
+// Whether the prompt kernel's tiles of 128 rows serve a call better than this file's of 16, by what
+// both take (measured, D = 128): here 0.27 us per SM and work tile of 16 rows x 32 tokens, over all
+// SMs, after 14 us; there 2.1 us per step of 128 tokens after 7 us, one CTA per SM, whose SMs
+// are not shared among splits of a sequence.  E.g. 8 KV heads, 8 heads each, 4,096 cached
+// tokens: 64 new tokens of 1 sequence 85 us here and 92 there, 128 new tokens 147 and 92; of 8
+// sequences 4 new tokens 51 and 76, 16 new tokens 141 and 79.
+bool wide_tiles(const AttnParams& p) {
+    const int64_t rows = (int64_t)p.c.max_q * p.group, units = (int64_t)p.c.batch * p.c.kv_heads;
+    const double sms = num_sms();
+    const double tiles = (double)units * (double)((rows + 15) / 16) * (double)((p.max_kv + A_TOK - 1) / A_TOK);
+    const int64_t waves = (prompt_ctas(p.c.batch, p.c.kv_heads, rows) + (int64_t)sms - 1) / (int64_t)sms;
+    return (double)waves * (7.0 + 2.1 * (double)((p.max_kv + 127) / 128)) < 14.0 + 0.27 * tiles / sms;
+}
+
+// 8 rows per tile where they hold all of a sequence's, else 16, or the prompt kernel's wide tiles.
 template <int FMT, int D>
 cudaError_t launch_rows(const AttnParams& p, cudaStream_t st) {
-    const int64_t rows = (int64_t)p.c.max_q * p.group;
-    if (rows <= 8) return launch_attention<FMT, D, 1>(p, st);
-    if (rows >= 64) return launch_prompt_attention(p, st);
+    if ((int64_t)p.c.max_q * p.group <= 8) return launch_attention<FMT, D, 1>(p, st);
+    if (wide_tiles(p)) return launch_prompt_attention(p, st);
     return launch_attention<FMT, D, 2>(p, st);
 }
 

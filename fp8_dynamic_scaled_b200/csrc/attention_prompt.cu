@@ -74,40 +74,55 @@ __device__ __forceinline__ int32_t sees_upto(const AttnParams& p, const Sequence
 }
 
 // ---------------------------------------------------------------- the converters
-// 16 codes of a row -> 32 bytes.  Thread t takes 16-byte chunk t % (D / 16) of rows t / (D / 16) + ..
+// A step's K (or V) codes in the four warps' registers: a thread takes one 16-byte chunk of every
+// 16th (D = 64: 32nd) row.  Eight neighbouring lanes take four chunks (64 elements) of two rows, so that
+// both their loads (64 contiguous bytes) and their swizzled stores (all banks once) are whole.
 template <int FMT, int D>
 struct Codes {
-    static constexpr int PER_ROW = D / 16;                      // chunks
-    static constexpr int STEP = 128 / PER_ROW;                  // rows between a thread's chunks (a multiple of 16)
+    static constexpr int STEP = 128 * 16 / D;                   // rows between a thread's chunks
     static constexpr int N = T_TOK / STEP;                      // chunks per thread
     uint4 v[N];
 
-    // `place`: the offset of 16 tokens, -1 for none, in the lane first + their number in the step; rows at
-    // or past `left` are zeros (those slots may hold anything).
-    __device__ __forceinline__ void load(const uint8_t* base, int64_t place, int32_t first, int32_t t, int32_t left) {
+    static __device__ __forceinline__ int32_t chunk(int32_t t) { return (t & 3) + (D == 128 ? 4 * ((t >> 3) & 1) : 0); }
+    static __device__ __forceinline__ int32_t row0(int32_t t) {
+        return D == 128 ? ((t >> 4) << 1) + ((t >> 2) & 1) : t >> 2;
+    }
+
+    // `at`: the first of 16 rows of codes in units of 16, -1 for none, in the lane first + their number in
+    // the step; rows at or past `left` are zeros (those slots may hold anything).
+    __device__ __forceinline__ void load(const uint8_t* base, int32_t at, int32_t first, int32_t t, int32_t left) {
+        const int32_t r0 = row0(t);
+        const uint8_t* mine = base + (r0 & 15) * D + chunk(t) * 16;
+        const bool whole = left >= T_TOK &&
+                           ((__ballot_sync(0xffffffffu, at >= 0) >> first) & ((1u << T_GROUPS) - 1)) == (1u << T_GROUPS) - 1;
+        if (whole) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int32_t row = t / PER_ROW + STEP * i;
-            const int64_t at = __shfl_sync(0xffffffffu, place, first + (row >> 4));
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (at >= 0 && row < left) v[i] = ld_v4(base + at + (row & 15) * D + (t % PER_ROW) * 16);
+            for (int i = 0; i < N; ++i) {
+                const int32_t g = __shfl_sync(0xffffffffu, at, first + (r0 >> 4) + i * (STEP / 16));
+                v[i] = ld_v4(mine + (int64_t)g * (16 * D));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int32_t g = __shfl_sync(0xffffffffu, at, first + (r0 >> 4) + i * (STEP / 16));
+                v[i] = make_uint4(0, 0, 0, 0);
+                if (g >= 0 && r0 + STEP * i < left) v[i] = ld_v4(mine + (int64_t)g * (16 * D));
+            }
         }
     }
     __device__ __forceinline__ void store(uint8_t* tile, int32_t t) const {
+        const int32_t c = chunk(t), r0 = row0(t);                // r0 + STEP i has the same low three bits
+        uint8_t* dst = tile + (c >> 2) * T_BLOCK + r0 * 128;
+        const uint32_t o0 = (((c & 3) * 2) ^ (r0 & 7)) << 4, o1 = o0 ^ 16;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const uint32_t row = t / PER_ROW + STEP * i, c = t % PER_ROW;
             uint4 lo, hi;
             half2x2_of<FMT>(v[i].x, lo.x, lo.y);
             half2x2_of<FMT>(v[i].y, lo.z, lo.w);
             half2x2_of<FMT>(v[i].z, hi.x, hi.y);
             half2x2_of<FMT>(v[i].w, hi.z, hi.w);
-            // two 16-byte chunks; lanes of the second block start with their second one, so that eight
-            // lanes write all banks once
-            uint8_t* dst = tile + (c >> 2) * T_BLOCK;
-            const uint32_t first = (c >> 2) & 1;
-            *reinterpret_cast<uint4*>(dst + swizzled(row, (c & 3) * 2 + first)) = first ? hi : lo;
-            *reinterpret_cast<uint4*>(dst + swizzled(row, (c & 3) * 2 + 1 - first)) = first ? lo : hi;
+            *reinterpret_cast<uint4*>(dst + o0 + i * STEP * 128) = lo;
+            *reinterpret_cast<uint4*>(dst + o1 + i * STEP * 128) = hi;
         }
     }
 };
@@ -121,7 +136,7 @@ __device__ __forceinline__ void convert(const AttnParams& p, const Unit& u, uint
     // Lane i holds the place and the scales of 16 tokens of 4 steps: those of number i % 8 in step
     // 4 B + i / 8 of batch B; the pages of the next batch are on the way meanwhile.
     int32_t next_page = -1;
-    int64_t place = -1;
+    int32_t place = -1;                       // in units of 16 rows of codes
     float ks = 0.0f, vs = 1.0f;
     auto fetch = [&](int32_t batch) {
         const int32_t tok = 16 * (32 * batch + lane);
@@ -136,7 +151,7 @@ __device__ __forceinline__ void convert(const AttnParams& p, const Unit& u, uint
         if (tok < u.sees) {
             if (next_page >= 0 && next_page < p.c.num_pages) {
                 const int64_t at = (int64_t)next_page * p.c.kv_heads + u.h;
-                place = (at * P + tok % P) * D;
+                place = (int32_t)((at * P + tok % P) >> 4);
                 ks = __ldg(p.c.k_scale + at);
                 vs = __ldg(p.c.v_scale + at);
             } else {
@@ -183,7 +198,6 @@ __device__ __forceinline__ void convert(const AttnParams& p, const Unit& u, uint
 template <int D>
 __device__ __forceinline__ void issue(const AttnParams& p, const Unit& u, uint32_t q16, uint32_t k16, uint32_t v16,
                                       uint32_t tmem, Bars* bars) {
-    const int lane = threadIdx.x & 31;
     // fp16 operands, fp32 accumulator, M = 128; scores: N = 128 tokens, both K-major; output: N = D,
     // V MN-major (bit 16)
     constexpr uint32_t idesc_s = (1u << 4) | ((uint32_t)(T_TOK >> 3) << 17) | ((uint32_t)(T_ROWS >> 4) << 24);
@@ -207,7 +221,7 @@ __device__ __forceinline__ void issue(const AttnParams& p, const Unit& u, uint32
     bool ok = warp_wait(&bars->qfull, 0, bars, p) && warp_wait(&bars->kfull[0], 0, bars, p);
     if (ok) {
         ptx::tc_fence_after();
-        if (lane == 0) {
+        if (ptx::elect_one()) {
             scores(0, 0);
             if (u.steps[1] > 0) scores(1, 0);
             ptx::mma_commit(&bars->kempty[0]);
@@ -224,20 +238,20 @@ __device__ __forceinline__ void issue(const AttnParams& p, const Unit& u, uint32
             ok = warp_wait(&bars->pfull[i], j & 1, bars, p);
             if (!ok) break;
             ptx::tc_fence_after();
-            if (lane == 0) {
+            if (ptx::elect_one()) {
                 output(i, buf, j > 0);
                 if (j + 1 < u.steps[i]) scores(i, nbuf);
                 else                    ptx::mma_commit(&bars->ofull[i]);
             }
             __syncwarp();
         }
-        if (ok && lane == 0) {
+        if (ok && ptx::elect_one()) {
             ptx::mma_commit(&bars->vempty[buf]);
             if (j + 1 < steps) ptx::mma_commit(&bars->kempty[nbuf]);
         }
         __syncwarp();
     }
-    if (lane == 0) {                          // issued MMAs finish before TMEM is freed
+    if (ptx::elect_one()) {                          // issued MMAs finish before TMEM is freed
         ptx::mma_commit(&bars->teardown);
         wait_drain(&bars->teardown, 0, p.c.status);
     }
@@ -245,28 +259,76 @@ __device__ __forceinline__ void issue(const AttnParams& p, const Unit& u, uint32
 }
 
 // ---------------------------------------------------------------- the rows
-// One step of a row: its 128 products s -> weights (fp16, over the products in tensor memory at
-// `ts`), the running maximum m (log2) and sum l; O at `to` follows a new maximum.  In units of
-// log2 a score is z = s f + a with f = qf s_k >= 0, a = log2 s_v per 16 tokens, so that a group's
-// largest score is that of its largest product.  EDGE: tokens at or past `left` are not seen.
-template <int D, bool EDGE>
-__device__ __forceinline__ void weights(const uint32_t (&s)[4][32], const GroupInfo* gi, int32_t left, float qf, float& m,
-                                        float& l, bool has_o, uint32_t ts, uint32_t to) {
-    float top = -INFINITY;                                 // with P_SHIFT in it
+// One step of a row: its 128 products (tensor memory, `ts`) -> weights (fp16, over them), the running
+// maximum m (log2) and sum l; O at `to` follows a new maximum.  In units of log2 a score is
+// z = s f + a with f = qf s_k >= 0, a = log2 s_v per 16 tokens, so that a group's largest
+// score is that of its largest product.  The products are read twice, 32 at a time with the next 32
+// on the way, for the maximum and for the weights: a read takes some 80 cycles for all 128, and
+// holding them leaves too few registers to keep the exponentials flowing.  EDGE: tokens at or past
+// `left` are not seen.
+template <bool EDGE>
+__device__ __forceinline__ float chunk_top(const uint32_t (&s)[32], const GroupInfo* gi, int32_t left, float qf) {
+    float top = -INFINITY;
 #pragma unroll
-    for (int g = 0; g < T_GROUPS; ++g) {
+    for (int h = 0; h < 2; ++h) {
         float g0 = -INFINITY, g1 = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-            const float x = __uint_as_float(s[g >> 1][(g & 1) * 16 + e]);
-            const float y = __uint_as_float(s[g >> 1][(g & 1) * 16 + e + 1]);
-            if (!EDGE || 16 * g + e < left) g0 = fmaxf(g0, x);
-            if (!EDGE || 16 * g + e + 1 < left) g1 = fmaxf(g1, y);
+        for (int e = 0; e < 16; e += 4) {
+            const float x[4] = {__uint_as_float(s[16 * h + e]), __uint_as_float(s[16 * h + e + 1]),
+                                __uint_as_float(s[16 * h + e + 2]), __uint_as_float(s[16 * h + e + 3])};
+            if (!EDGE) {
+                g0 = fmaxf(fmaxf(g0, x[0]), x[1]);
+                g1 = fmaxf(fmaxf(g1, x[2]), x[3]);
+            } else {
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    if (16 * h + e + y < left) g0 = fmaxf(g0, x[y]);
+            }
         }
         g0 = fmaxf(g0, g1);
-        const float2 q = *reinterpret_cast<const float2*>(&gi[g]);
+        const float2 q = *reinterpret_cast<const float2*>(&gi[h]);
         const float z = fmaf(g0, qf * q.x, q.y);
         top = fmaxf(top, EDGE && g0 == -INFINITY ? -INFINITY : z);
+    }
+    return top;
+}
+template <bool EDGE>
+__device__ __forceinline__ void chunk_weights(const uint32_t (&s)[32], const GroupInfo* gi, int32_t left, float qf, float base,
+                                              float& l, uint32_t (&w)[16]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float4 q = *reinterpret_cast<const float4*>(&gi[h]);
+        const float2 f2 = make_float2(qf * q.x, qf * q.x), a2 = make_float2(q.y - base, q.y - base);
+        float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+            float2 z = fma2_rn(make_float2(__uint_as_float(s[16 * h + e]), __uint_as_float(s[16 * h + e + 1])), f2, a2);
+            if (EDGE && 16 * h + e >= left) z.x = -INFINITY;
+            if (EDGE && 16 * h + e + 1 >= left) z.y = -INFINITY;
+            const float2 y = make_float2(ex2(z.x), ex2(z.y));
+            part[(e >> 1) & 1] = add2_rn(part[(e >> 1) & 1], y);
+            w[8 * h + e / 2] = pack_half2(y.x, y.y);
+        }
+        const float2 sum = add2_rn(part[0], part[1]);
+        l = fmaf(sum.x + sum.y, q.z, l);
+    }
+}
+
+template <int D, bool EDGE>
+__device__ __forceinline__ void weights(const GroupInfo* gi, int32_t left, float qf, float& m, float& l, bool has_o,
+                                        uint32_t ts, uint32_t to) {
+    uint32_t s0[32], s1[32];
+    ptx::tmem_ld_32x32b_x32(ts, s0);
+    ptx::tmem_ld_wait();
+    float top = -INFINITY;                                 // with P_SHIFT in it
+#pragma unroll
+    for (int c = 0; c < 4; c += 2) {
+        ptx::tmem_ld_32x32b_x32(ts + 32 * (c + 1), s1);
+        top = fmaxf(top, chunk_top<EDGE>(s0, gi + 2 * c, left - 32 * c, qf));
+        ptx::tmem_ld_wait();
+        ptx::tmem_ld_32x32b_x32(ts + 32 * ((c + 2) & 3), s0);      // the last: the first again
+        top = fmaxf(top, chunk_top<EDGE>(s1, gi + 2 * c + 2, left - 32 * c - 32, qf));
+        ptx::tmem_ld_wait();
     }
     const bool far = m == -INFINITY ? top > -INFINITY : top > m + (P_SHIFT + P_LAG);
     if (__any_sync(0xffffffffu, far)) {
@@ -288,27 +350,16 @@ __device__ __forceinline__ void weights(const uint32_t (&s)[4][32], const GroupI
     }
     const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < 4; c += 2) {
         uint32_t w[16];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int g = 2 * c + h;
-            const float4 q = *reinterpret_cast<const float4*>(&gi[g]);
-            const float2 f2 = make_float2(qf * q.x, qf * q.x), a2 = make_float2(q.y - base, q.y - base);
-            float2 part = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-                float2 z = fma2_rn(make_float2(__uint_as_float(s[c][16 * h + e]), __uint_as_float(s[c][16 * h + e + 1])),
-                                   f2, a2);
-                if (EDGE && 16 * g + e >= left) z.x = -INFINITY;
-                if (EDGE && 16 * g + e + 1 >= left) z.y = -INFINITY;
-                const float2 y = make_float2(ex2(z.x), ex2(z.y));
-                part = add2_rn(part, y);
-                w[8 * h + e / 2] = pack_half2(y.x, y.y);
-            }
-            l = fmaf(part.x + part.y, q.z, l);
-        }
-        ptx::tmem_st_32x32b_x16(ts + 16 * c, w);
+        ptx::tmem_ld_32x32b_x32(ts + 32 * (c + 1), s1);
+        chunk_weights<EDGE>(s0, gi + 2 * c, left - 32 * c, qf, base, l, w);
+        ptx::tmem_ld_wait();
+        ptx::tmem_st_32x32b_x16(ts + 16 * c, w);           // over products that have been read
+        if (c == 0) ptx::tmem_ld_32x32b_x32(ts + 64, s0);
+        chunk_weights<EDGE>(s1, gi + 2 * c + 2, left - 32 * c - 32, qf, base, l, w);
+        if (c == 0) ptx::tmem_ld_wait();
+        ptx::tmem_st_32x32b_x16(ts + 16 * c + 16, w);
     }
 }
 
@@ -355,16 +406,12 @@ __device__ __forceinline__ void rows(const AttnParams& p, const Unit& u, uint8_t
     for (int32_t j = 0; j < u.steps[i]; ++j) {
         if (!warp_wait(&bars->sfull[i], j & 1, bars, p)) return;
         ptx::tc_fence_after();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x32(ts + 32 * c, s[c]);
-        ptx::tmem_ld_wait();
         const GroupInfo* gi = info[j & 3];
         const int32_t left = limit - j * T_TOK;
         if (least - j * T_TOK < T_TOK)                     // some row of the warp ends in this step
-            weights<D, true>(s, gi, left, qf, m, l, j > 0, ts, to);
+            weights<D, true>(gi, left, qf, m, l, j > 0, ts, to);
         else
-            weights<D, false>(s, gi, left, qf, m, l, j > 0, ts, to);
+            weights<D, false>(gi, left, qf, m, l, j > 0, ts, to);
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         __syncwarp();
@@ -445,15 +492,20 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_prompt_attention_kernel(const
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bars->tmem_slot);
-    // registers: 128 a thread at launch, 512 for the four warpgroups together; 40 + 104 + 2 * 184 = 512
+    // registers: 128 a thread at launch, 512 for the four warpgroups together; 56 + 120 + 2 * 168 = 512
     if (warp < 4) {
-        ptx::regs_dec<40>();
-        if (warp == 0) issue<D>(p, u, ptx::smem_u32(q16), ptx::smem_u32(k16), ptx::smem_u32(v16), tmem, bars);
+        ptx::regs_dec<56>();
+        if (warp == 0) {
+            // the same in all lanes, and known to be: the MMAs take their operands from uniform registers
+            auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+            issue<D>(p, u, uniform(ptx::smem_u32(q16)), uniform(ptx::smem_u32(k16)), uniform(ptx::smem_u32(v16)),
+                     uniform(tmem), bars);
+        }
     } else if (warp < 8) {
-        ptx::regs_dec<104>();
+        ptx::regs_dec<120>();
         convert<FMT, D>(p, u, k16, v16, info, bars);
     } else {
-        ptx::regs_inc<184>();
+        ptx::regs_inc<168>();
         rows<D>(p, u, q16, info, tmem, bars);
     }
     ptx::tc_fence_before();

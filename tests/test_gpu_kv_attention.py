@@ -294,3 +294,9 @@ def test_many_long_sequences(group):
     lens = [700 + 97 * (i % 13) for i in range(40)]
     lens[3], lens[35] = 9001, 6400
     check(Paged(lens, 4, 64, 128, 0, seed=19), [1] * 40, group)
+
+
+@pytest.mark.parametrize("group,dim,fmt", [(8, 128, 0), (16, 64, 1), (7, 128, 1)])
+def test_a_few_tokens_over_long_caches(group, dim, fmt):
+    """Several row tiles of 16 per sequence, each split over CTAs."""
+    check(Paged([20000, 3000, 9, 0], 2, 64, dim, fmt, seed=20), [8, 5, 9, 0], group)
