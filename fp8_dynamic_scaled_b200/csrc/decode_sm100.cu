@@ -15,7 +15,7 @@
 //     at most 128 rows.  Rows of the 128-row tile past a chunk are not loaded; their
 //     accumulator lanes are never read.  No partial sums cross CTAs;
 //   - HBM is read in long runs: a stage holds KBS (4, or 3 with more tokens) K blocks
-//     of 128 bytes of the chunk, loaded as 64-row (and 16-row) TMA boxes issued
+//     of 128 bytes of the chunk, loaded as 64-row (and 32- and 16-row) TMA boxes issued
 //     row-group by row-group, so each row's KBS consecutive blocks are requested back
 //     to back.  (Measured on this part with loads alone: 128-row x 128-byte boxes
 //     stream at ~4.8 TB/s, 64 rows x 4 consecutive blocks at ~6.2 TB/s.)  The boxes
@@ -77,7 +77,8 @@ constexpr int D_THREADS = 32 * (2 + D_EPI_WARPS);
 template <int EXT>
 __global__ void __launch_bounds__(D_THREADS, 1)
 fp8_decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW64,
-                  const __grid_constant__ CUtensorMap tmW16, const GemmParams p, const DecodeParams d) {
+                  const __grid_constant__ CUtensorMap tmW32, const __grid_constant__ CUtensorMap tmW16,
+                  const GemmParams p, const DecodeParams d) {
     constexpr int EPI_WARPS = D_EPI_WARPS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -112,6 +113,7 @@ fp8_decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&tmX);
         ptx::prefetch_tmap(&tmW64);
+        ptx::prefetch_tmap(&tmW32);
         ptx::prefetch_tmap(&tmW16);
     }
     if (warp == 1) {
@@ -142,11 +144,11 @@ fp8_decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                     ptx::mbar_arrive_expect_tx(&full[stage], (uint32_t)kbs * (uint32_t)(w + d.nt) * BK);
                     // row group by row group, each group's K blocks back to back
                     for (int32_t r = 0; r < w;) {
-                        const bool big = w - r >= 64;
+                        const int32_t box = w - r >= 64 ? 64 : w - r >= 32 ? 32 : D_UNIT;
+                        const CUtensorMap* tm = box == 64 ? &tmW64 : box == 32 ? &tmW32 : &tmW16;
                         for (int32_t b = 0; b < kbs; ++b)
-                            ptx::tma_load_2d(st + b * D_TILE_BYTES + r * BK, big ? &tmW64 : &tmW16, &full[stage],
-                                             (kb0 + b) * BK, n0 + r);
-                        r += big ? 64 : D_UNIT;
+                            ptx::tma_load_2d(st + b * D_TILE_BYTES + r * BK, tm, &full[stage], (kb0 + b) * BK, n0 + r);
+                        r += box;
                     }
                 }
                 if (x_part)
@@ -227,11 +229,21 @@ fp8_decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             int32_t n0, w;
             decode_chunk(range, j, n0, w);
             const uint32_t buf = acc_it & 1u, use = acc_it >> 1;
-            if (!wait_bounded(&tfull[buf], use & 1u, abort_flag, p.status, p.wait_ns)) break;
-            ptx::tc_fence_after();
             const int32_t r = quarter * 32 + lane;                 // row of the chunk
             const int32_t n = n0 + r;
             const bool valid = r < w && n < p.N;
+            // the residual of a 16-token group is fetched ahead of its use (the first one's while the
+            // products are computed): its loads may alias Y, so they would otherwise wait for
+            // each other's stores
+            uint32_t res[16];
+            auto load_residual = [&](int32_t c0) {
+#pragma unroll
+                for (int t = 0; t < 16; ++t)
+                    res[t] = valid && c0 + t < p.M ? p.res[(int64_t)(c0 + t) * p.ldres + n] : 0u;
+            };
+            if (EXT == EPI_ACT && p.res) load_residual(16 * th);
+            if (!wait_bounded(&tfull[buf], use & 1u, abort_flag, p.status, p.wait_ns)) break;
+            ptx::tc_fence_after();
             if (quarter * 32 < w) {                                // warp-uniform
                 const float sw = valid ? __ldg(p.sb + (int64_t)n * p.sb_stride) : 0.0f;
                 float bias = 0.0f;
@@ -250,7 +262,7 @@ fp8_decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                             float f[1] = {v};
                             activate(p.activation, f);
                             v = f[0];
-                            if (p.res) v = __fadd_rn(v, bf16bits_to_float(p.res[(int64_t)m * p.ldres + n]));
+                            if (p.res) v = __fadd_rn(v, bf16bits_to_float(res[t]));
                         }
                         const uint32_t yb = pack_bf16x2(v, 0.0f) & 0xFFFFu;
                         if (!EXT || p.write_y) p.y[(int64_t)m * p.ldy + n] = (uint16_t)yb;
@@ -265,6 +277,7 @@ fp8_decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                             }
                         }
                     }
+                    if (EXT == EPI_ACT && p.res && c0 + 32 < p.M) load_residual(c0 + 32);
                 }
             }
             ptx::tc_fence_before();
@@ -295,10 +308,12 @@ static cudaError_t launch_decode_t(const GemmArgs& g, GemmParams p, cudaStream_t
     d.kbs = d.nt <= 16 ? D_MAX_KBS : 3;
     d.stage_bytes = (uint32_t)d.kbs * (D_TILE_BYTES + (uint32_t)d.nt * BK);
     d.stages = (int32_t)std::min<uint32_t>(D_MAX_STAGES, (D_SMEM - 1024 - D_BAR_BYTES) / d.stage_bytes);
-    CUtensorMap tx, t64, t16;
+    CUtensorMap tx, t64, t32, t16;
     if (!make_map_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a, (uint64_t)g.K, (uint64_t)g.M, (uint64_t)g.K, BK,
                      (uint32_t)d.nt, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_map_2d(&t64, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.b, (uint64_t)g.K, (uint64_t)g.N, (uint64_t)g.K, BK, 64,
+                     CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map_2d(&t32, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.b, (uint64_t)g.K, (uint64_t)g.N, (uint64_t)g.K, BK, 32,
                      CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_map_2d(&t16, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.b, (uint64_t)g.K, (uint64_t)g.N, (uint64_t)g.K, BK, 16,
                      CU_TENSOR_MAP_SWIZZLE_128B))
@@ -318,7 +333,10 @@ static cudaError_t launch_decode_t(const GemmArgs& g, GemmParams p, cudaStream_t
     // M = 128 weight rows, N = nt tokens
     p.idesc = (1u << 4) | ((uint32_t)g.fmt_b << 7) | ((uint32_t)g.fmt_a << 10) | ((uint32_t)(d.nt >> 3) << 17) |
               ((uint32_t)(D_TILE >> 4) << 24);
-    const int grid = std::max(1, std::min(d.units, num_sms()));
+    // equal shares: as many units for every CTA as the largest share has anyway (N = 8192, K = 28672:
+    // 128 CTAs of 64 rows 52 us, 148 CTAs of 48 or 64 rows 77 us)
+    const int per = (d.units + num_sms() - 1) / num_sms();
+    const int grid = std::max(1, (d.units + per - 1) / per);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(D_THREADS);
@@ -329,7 +347,7 @@ static cudaError_t launch_decode_t(const GemmArgs& g, GemmParams p, cudaStream_t
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.pdl ? 1 : 0;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_decode_kernel<EXT>, tx, t64, t16, p, d);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_decode_kernel<EXT>, tx, t64, t32, t16, p, d);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }

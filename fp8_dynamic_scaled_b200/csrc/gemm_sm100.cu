@@ -325,6 +325,12 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             tile_coords(p, t, mb, nb);
             const int32_t row = mb * BM + quarter * 32 + lane;
             const int32_t y_row0 = mb * BM + quarter * 32;
+            ResidualChunk rc;
+            uint32_t res[16];
+            // the residual of a tile's first chunk is fetched while its products are computed (not by the
+            // variants that keep 128 accumulators in registers), of each next one while the one
+            // before is written out
+            if (V == V_ROWSCALE && EXT == EPI_ACT && p.res) rc.load(p, nb * BN, y_row0, lane);
             if (V == V_ROWSCALE) {
                 const uint32_t buf = acc_it % C::ACC_BUFS, use = acc_it / C::ACC_BUFS;
                 if (!wait_bounded(&tfull[buf], use & 1u, abort_flag, p.status, p.wait_ns)) { ok = false; break; }
@@ -342,9 +348,17 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     }
                     const int32_t n0 = nb * BN + c * 32;
                     uint32_t w[16];
-                    rowscale_chunk<EXT>(p, es, r, sx, n0, p.N, row, w);
+                    uint8_t* b = ybuf + (store_it % C::STAGE_BUFS) * 2048;
+                    if (EXT && p.turns) {
+                        if (lane == 0) ptx::bulk_wait_read<C::STAGE_BUFS - 1>();
+                        __syncwarp();
+                    }
+                    if (EXT == EPI_ACT && p.res) {
+                        rc.turn(b, lane, res);
+                        if (c + 1 < BN / 32) rc.load(p, n0 + 32, y_row0, lane);
+                    }
+                    rowscale_chunk<EXT>(p, es, r, res, sx, n0, p.N, row, w, b);
                     if (n0 < p.N && (!EXT || p.write_y)) {
-                        uint8_t* b = ybuf + (store_it % C::STAGE_BUFS) * 2048;
                         if (lane == 0) ptx::bulk_wait_read<C::STAGE_BUFS - 1>();
                         __syncwarp();
                         store_chunk(&tmY, b, w, n0, y_row0, lane, p, p.N);
@@ -415,10 +429,20 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     }
                 }
                 if (!ok) break;
+                if (EXT == EPI_ACT && p.res) rc.load(p, nb * BN + half * 128, y_row0, lane);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int32_t n0 = nb * BN + half * 128 + c * 32;
                     uint32_t w[16];
+                    uint8_t* b = ybuf + (store_it % C::STAGE_BUFS) * 2048;
+                    if (EXT && p.turns) {
+                        if (lane == 0) ptx::bulk_wait_read<C::STAGE_BUFS - 1>();
+                        __syncwarp();
+                    }
+                    if (EXT == EPI_ACT && p.res) {
+                        rc.turn(b, lane, res);
+                        if (c < 3) rc.load(p, n0 + 32, y_row0, lane);
+                    }
                     if (!EXT) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(acc[c * 16 + j].x, acc[c * 16 + j].y);
@@ -429,10 +453,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                             f[2 * j] = acc[c * 16 + j].x;
                             f[2 * j + 1] = acc[c * 16 + j].y;
                         }
-                        epi_chunk<EXT>(p, es, f, n0, p.N, row, w);
+                        epi_chunk<EXT>(p, es, f, res, n0, p.N, row, w, b);
                     }
                     if (n0 < p.N && (!EXT || p.write_y)) {
-                        uint8_t* b = ybuf + (store_it % C::STAGE_BUFS) * 2048;
                         if (lane == 0) ptx::bulk_wait_read<C::STAGE_BUFS - 1>();
                         __syncwarp();
                         store_chunk(&tmY, b, w, n0, y_row0, lane, p, p.N);
@@ -451,10 +474,20 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&tempty[0]);
                 ++acc_it;
+                if (EXT == EPI_ACT && p.res) rc.load(p, nb * BN + half * 128, y_row0, lane);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int32_t n0 = nb * BN + half * 128 + c * 32;
                     uint32_t w[16];
+                    uint8_t* b = ybuf + (store_it % C::STAGE_BUFS) * 2048;
+                    if (EXT && p.turns) {
+                        if (lane == 0) ptx::bulk_wait_read<C::STAGE_BUFS - 1>();
+                        __syncwarp();
+                    }
+                    if (EXT == EPI_ACT && p.res) {
+                        rc.turn(b, lane, res);
+                        if (c < 3) rc.load(p, n0 + 32, y_row0, lane);
+                    }
                     if (!EXT) {
 #pragma unroll
                         for (int j = 0; j < 32; j += 2)
@@ -463,10 +496,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         float f[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(r[c][j]);
-                        epi_chunk<EXT>(p, es, f, n0, p.N, row, w);
+                        epi_chunk<EXT>(p, es, f, res, n0, p.N, row, w, b);
                     }
                     if (n0 < p.N && (!EXT || p.write_y)) {
-                        uint8_t* b = ybuf + (store_it % C::STAGE_BUFS) * 2048;
                         if (lane == 0) ptx::bulk_wait_read<C::STAGE_BUFS - 1>();
                         __syncwarp();
                         store_chunk(&tmY, b, w, n0, y_row0, lane, p, p.N);
@@ -659,6 +691,9 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             const int32_t y_row0 = mb * P_BM + (int32_t)rank * 128 + quarter * 32;
             const int32_t row = y_row0 + lane;
             const uint32_t buf = acc_it & 1u, use = acc_it >> 1;
+            ResidualChunk rc;
+            uint32_t res[16];
+            if (EXT == EPI_ACT && p.res) rc.load(p, nb * BN, y_row0, lane);      // see fp8_gemm_kernel
             if (!wait_bounded(&tfull[buf], use & 1u, abort_flag, p.status, p.wait_ns)) { ok = false; break; }
             ptx::tc_fence_after();
             const float sx = row < p.M ? __ldg(p.sa + (int64_t)row * p.sa_stride) : 0.0f;
@@ -674,9 +709,17 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 }
                 const int32_t n0 = nb * BN + c * 32;
                 uint32_t w[16];
-                rowscale_chunk<EXT>(p, es, r, sx, n0, p.N, row, w);
+                uint8_t* b = ybuf + (store_it % S::STAGE_BUFS) * 2048;
+                if (EXT && p.turns) {
+                    if (lane == 0) ptx::bulk_wait_read<S::STAGE_BUFS - 1>();
+                    __syncwarp();
+                }
+                if (EXT == EPI_ACT && p.res) {
+                    rc.turn(b, lane, res);
+                    if (c + 1 < BN / 32) rc.load(p, n0 + 32, y_row0, lane);
+                }
+                rowscale_chunk<EXT>(p, es, r, res, sx, n0, p.N, row, w, b);
                 if (n0 < p.N && (!EXT || p.write_y)) {
-                    uint8_t* b = ybuf + (store_it % S::STAGE_BUFS) * 2048;
                     if (lane == 0) ptx::bulk_wait_read<S::STAGE_BUFS - 1>();
                     __syncwarp();
                     store_chunk(&tmY, b, w, n0, y_row0, lane, p, p.N);
@@ -836,6 +879,7 @@ static void set_epilogue(const GemmArgs& g, GemmParams& p) {
     p.res = g.residual;
     p.ldres = g.ldres;
     p.res_vec = (g.ldres % 8 == 0 && (reinterpret_cast<uintptr_t>(g.residual) & 15u) == 0) ? 1 : 0;
+    p.turns = (g.residual != nullptr || (g.yq != nullptr && !p.yq_vec)) ? 1 : 0;
     p.write_y = g.y != nullptr ? 1 : 0;
     if (!p.write_y) p.y_direct = 1;
 }
@@ -923,8 +967,15 @@ __global__ void __launch_bounds__(256) epi_zero_k_kernel(const GemmParams p) {
         float f[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) f[j] = 0.0f;
-        uint32_t w[16];
-        epi_chunk<EXT>(p, es, f, n0, p.N, row, w);
+        uint32_t w[16], res[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int32_t n = n0 + 2 * j;
+            const uint16_t* src = p.res + (int64_t)row * p.ldres + n;
+            const bool real = EXT == EPI_ACT && p.res && row < p.M;
+            res[j] = (real && n < p.N ? src[0] : 0u) | ((real && n + 1 < p.N ? (uint32_t)src[1] : 0u) << 16);
+        }
+        epi_chunk<EXT>(p, es, f, res, n0, p.N, row, w);
         if (p.write_y && row < p.M) {
             uint16_t* dst = p.y + (int64_t)row * p.ldy;
 #pragma unroll
