@@ -139,6 +139,8 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
+        if torch.cuda.is_initialized():       # what current_stream() looks up, without building its object
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -311,12 +313,17 @@ def fp8_linear_forward_ex(x, x_fmt, x_mode, w, w_scale, w_mode, w_fmt, y, worksp
 
 
 def _epilogue_act(M, N, bias, activation, residual, amax, yq, yq_scale, yq_fmt):
-    if residual is not None and (residual.dtype != torch.bfloat16 or tuple(residual.shape) != (M, N)
-                                 or (N > 1 and residual.stride(1) != 1)):
-        raise TypeError("residual must be bf16 [M, N] with unit column stride")
-    base = _epilogue(N, bias, amax, yq, yq_scale, yq_fmt) or fp8_epilogue_t()
-    ldres = 0 if residual is None else (residual.stride(0) if M > 1 else N)
-    return fp8_epilogue_act_t(base, activation, _ptr(residual), ldres)
+    epi = fp8_epilogue_act_t()
+    base = _epilogue(N, bias, amax, yq, yq_scale, yq_fmt)
+    if base is not None:
+        epi.base = base
+    epi.activation = activation
+    if residual is not None:
+        stride = residual.stride()
+        if residual.dtype is not torch.bfloat16 or residual.shape != (M, N) or (N > 1 and stride[1] != 1):
+            raise TypeError("residual must be bf16 [M, N] with unit column stride")
+        epi.residual_dev, epi.ldres = residual.data_ptr(), stride[0] if M > 1 else N
+    return epi
 
 
 def fp8_scaled_gemm_act(a, a_scale, a_mode, fmt_a, b, b_scale, b_mode, fmt_b, y, *, bias=None,
@@ -356,9 +363,10 @@ def fp8_linear_forward_act(x, x_fmt, x_mode, w, w_scale, w_mode, w_fmt, y, works
 
 def _rows_of(t, name, rows, cols):
     """Row stride of a bf16 [rows, cols] tensor with unit column stride."""
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != (rows, cols) or (t.numel() and t.stride(1) != 1):
+    stride = t.stride()
+    if t.dtype is not torch.bfloat16 or t.shape != (rows, cols) or (rows and cols and stride[1] != 1):
         raise TypeError(f"{name} must be bf16 [{rows}, {cols}] with unit column stride")
-    return t.stride(0) if rows > 1 and cols else cols
+    return stride[0] if rows > 1 and cols else cols
 
 
 def fp8_rmsnorm_quantize(x, weight, eps, fmt, mode, q, scale, *, residual=None, sum_out=None, y=None, amax=None,
@@ -374,14 +382,17 @@ def fp8_rmsnorm_quantize(x, weight, eps, fmt, mode, q, scale, *, residual=None, 
     lds = 0 if sum_out is None else _rows_of(sum_out, "sum_out", rows, cols)
     if weight is not None and (weight.dtype != torch.bfloat16 or weight.numel() != cols or not weight.is_contiguous()):
         raise TypeError("weight must be bf16 [cols]")
-    if q.dtype != torch.uint8 or tuple(q.shape) != (rows, cols) or not q.is_contiguous():
+    if q.dtype is not torch.uint8 or q.shape != (rows, cols) or not q.is_contiguous():
         raise TypeError("q must be dense uint8 [rows, cols]")
-    want = torch.uint8 if mode == FP8_SCALE_MX32 else torch.float32
-    if scale.dtype != want or not scale.is_contiguous() or (mode in _SCALE_MODES and
-                                                            scale.numel() < _numel(scale_shape(mode, rows, cols))):
+    mx = mode == FP8_SCALE_MX32
+    need = rows if mode == FP8_SCALE_ROW else rows * (cols // 32) if mx else rows * -(-cols // 128) \
+        if mode == FP8_SCALE_BLOCK_1x128 else 1
+    if scale.dtype is not (torch.uint8 if mx else torch.float32) or not scale.is_contiguous() or scale.numel() < need:
         raise TypeError("scale must be a dense buffer of the mode's scales")
-    if y is not None and (y.dtype != torch.bfloat16 or tuple(y.shape) != (rows, cols) or not y.is_contiguous()):
+    if y is not None and (y.dtype is not torch.bfloat16 or y.shape != (rows, cols) or not y.is_contiguous()):
         raise TypeError("y must be dense bf16 [rows, cols]")
+    if amax is not None and amax.dtype is not torch.float32:
+        raise TypeError("amax must be fp32")
     rc = _lib.fp8_rmsnorm_quantize(_ptr(x), rows, cols, ldx, _ptr(residual), ldr, _ptr(sum_out), lds, _ptr(weight),
                                    float(eps), fmt, mode, _ptr(amax), _ptr(q), _ptr(scale), _ptr(y), _ptr(dev_status),
                                    _stream(stream))
@@ -414,31 +425,34 @@ class KVCache:
 
     def view(self, page_table, kv_lens):
         """The C descriptor with a batch's page table [batch, max_pages] and lengths [batch] (int32)."""
-        if page_table.dtype != torch.int32 or page_table.dim() != 2 or (page_table.numel() and page_table.stride(1) != 1):
+        shape, stride = page_table.shape, page_table.stride()
+        if page_table.dtype is not torch.int32 or len(shape) != 2 or (shape[0] and shape[1] and stride[1] != 1):
             raise TypeError("page_table must be int32 [batch, max_pages] with unit column stride")
-        batch, pages = page_table.shape
-        if kv_lens.dtype != torch.int32 or kv_lens.dim() != 1 or kv_lens.shape[0] != batch or not kv_lens.is_contiguous():
+        batch, pages = shape
+        if kv_lens.dtype is not torch.int32 or kv_lens.shape != (batch,) or not kv_lens.is_contiguous():
             raise TypeError("kv_lens must be int32 [batch]")
         c = self.c
         c.page_table_dev, c.max_pages = page_table.data_ptr(), pages
-        c.table_stride = page_table.stride(0) if batch > 1 and pages else pages
+        c.table_stride = stride[0] if batch > 1 and pages else pages
         c.kv_lens_dev, c.batch = kv_lens.data_ptr(), batch
         return c
 
 
 def _head_rows(t, name, heads, dim):
     """Token stride of a bf16 [tokens, heads, dim] tensor whose heads are dense within a token."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or \
-            (t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim))):
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not torch.bfloat16 or len(shape) != 3 or shape[1] != heads or shape[2] != dim or \
+            (shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != dim))):
         raise TypeError(f"{name} must be bf16 [tokens, {heads}, {dim}], its heads dense within a token")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    return stride[0] if shape[0] > 1 else heads * dim
 
 
 def _cu_q(cu_q, batch):
-    if cu_q is not None and (cu_q.dtype != torch.int32 or cu_q.dim() != 1 or cu_q.shape[0] != batch + 1
-                             or not cu_q.is_contiguous()):
+    if cu_q is None:
+        return None
+    if cu_q.dtype is not torch.int32 or cu_q.shape != (batch + 1,) or not cu_q.is_contiguous():
         raise TypeError("cu_q must be int32 [batch + 1]")
-    return _ptr(cu_q)
+    return cu_q.data_ptr()
 
 
 def fp8_kv_append(k, v, cache: KVCache, page_table, kv_lens, *, cu_q=None, max_q_len=1, dev_status=None, stream=None):
@@ -468,13 +482,14 @@ def fp8_kv_attention(q, cache: KVCache, page_table, kv_lens, out, *, max_kv_len,
                      softmax_scale=None, workspace=None, dev_status=None, stream=None):
     """Causal attention of q (bf16 [tokens, q_heads, head_dim]) over the cache into out (the same shape);
     softmax_scale defaults to head_dim ** -0.5."""
-    if q.dim() != 3 or tuple(out.shape) != tuple(q.shape):
+    if q.dim() != 3 or out.shape != q.shape:
         raise TypeError("q and out must be bf16 [tokens, q_heads, head_dim]")
-    ldq = _head_rows(q, "q", q.shape[1], cache.head_dim)
-    ldo = _head_rows(out, "out", q.shape[1], cache.head_dim)
+    tokens, heads, dim = q.shape
+    ldq = _head_rows(q, "q", heads, cache.head_dim)
+    ldo = _head_rows(out, "out", heads, cache.head_dim)
     c = cache.view(page_table, kv_lens)
-    scale = cache.head_dim ** -0.5 if softmax_scale is None else float(softmax_scale)
-    _check(_lib.fp8_kv_attention(ctypes.byref(c), _ptr(q), ldq, q.shape[1], q.shape[0], _cu_q(cu_q, c.batch), max_q_len,
+    scale = dim ** -0.5 if softmax_scale is None else float(softmax_scale)
+    _check(_lib.fp8_kv_attention(ctypes.byref(c), _ptr(q), ldq, heads, tokens, _cu_q(cu_q, c.batch), max_q_len,
                                  max_kv_len, scale, _ptr(out), ldo, _ptr(dev_status), _ptr(workspace),
                                  _nbytes(workspace), _stream(stream)), "fp8_kv_attention")
 
@@ -511,17 +526,6 @@ def fp8_linear_forward_noalloc(x, x_fmt, x_mode, w, w_scale, w_mode, w_fmt, y, *
 
 
 # ------------------------------------------------------------------ allocation helpers
-_SCALE_MODES = (FP8_SCALE_TENSOR, FP8_SCALE_ROW, FP8_SCALE_BLOCK_1x128, FP8_SCALE_BLOCK_128x128, FP8_SCALE_MX32,
-                FP8_SCALE_DELAYED)
-
-
-def _numel(shape) -> int:
-    n = 1
-    for d in shape:
-        n *= d
-    return n
-
-
 def scale_shape(mode: int, rows: int, cols: int):
     if mode in (FP8_SCALE_TENSOR, FP8_SCALE_DELAYED):
         return (1,)

@@ -87,16 +87,20 @@ __device__ __forceinline__ int64_t head_tiles(const AttnParams& p, const Sequenc
 
 // This CTA's range of the work and where it begins: the whole CTA calls it.
 struct Range {
-    int64_t lo, total;
+    int64_t lo;
     int32_t n;                        // tiles of the range
-    int32_t ctas;
+    int64_t each;                     // tiles of every CTA, one more for the first `extra`
+    int32_t extra;
+    // The CTA that has tile x of the whole list.
+    __device__ __forceinline__ int32_t cta_of(int64_t x) const {
+        const int64_t longer = extra * (each + 1);
+        return (int32_t)(x < longer ? x / (each + 1) : extra + (x - longer) / each);
+    }
 };
 struct Start {
     int64_t inside;                   // tiles of sequence b before the range
     int32_t b;
 };
-
-__device__ __forceinline__ int64_t range_begin(int64_t total, int32_t ctas, int32_t i) { return total * i / ctas; }
 
 template <class S>
 __device__ Range find_range(const AttnParams& p, Start* start, int64_t* sums /* [32] */) {
@@ -118,17 +122,18 @@ __device__ Range find_range(const AttnParams& p, Start* start, int64_t* sums /* 
     if (lane == 31) sums[warp] = incl;
     __syncthreads();
     Range r;
-    int64_t before = 0;
-    r.total = 0;
+    int64_t before = 0, total = 0;
     for (int w = 0; w < nw; ++w) {
         if (w < warp) before += sums[w];
-        r.total += sums[w];
+        total += sums[w];
     }
     // a CTA's warps share its tiles: fewer CTAs when there is not one tile for each warp
-    r.ctas = (int32_t)max((int64_t)1, min((int64_t)gridDim.x, (r.total + S::WARPS - 1) / S::WARPS));
+    const int32_t ctas = (int32_t)max((int64_t)1, min((int64_t)gridDim.x, (total + S::WARPS - 1) / S::WARPS));
     const int32_t i = (int32_t)blockIdx.x;
-    r.lo = i < r.ctas ? range_begin(r.total, r.ctas, i) : r.total;
-    r.n = i < r.ctas ? (int32_t)(range_begin(r.total, r.ctas, i + 1) - r.lo) : 0;
+    r.each = total / ctas;
+    r.extra = (int32_t)(total - r.each * ctas);
+    r.lo = i < ctas ? r.each * i + min(i, r.extra) : total;
+    r.n = i < ctas ? (int32_t)r.each + (i < r.extra ? 1 : 0) : 0;
     const int64_t first = before + incl - mine;
     if (r.lo >= first && r.lo < first + mine) {
         int64_t at = first;
@@ -584,10 +589,7 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const Range& ran
         n += count;
         if (n >= range.n && !whole && off == 0) {          // begins here, ends in a later CTA
             const int64_t last = range.lo + n - count + u.tiles - 1;
-            int32_t i = (int32_t)(last * range.ctas / range.total);
-            while (range_begin(range.total, range.ctas, i + 1) <= last) ++i;
-            while (range_begin(range.total, range.ctas, i) > last) --i;
-            goes_on = make_int4(u.b, u.h * p.row_tiles + u.rt, slot, i);
+            goes_on = make_int4(u.b, u.h * p.row_tiles + u.rt, slot, range.cta_of(last));
         }
         off = 0;
         if (n < range.n) u.next(p);

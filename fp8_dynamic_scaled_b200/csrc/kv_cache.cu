@@ -6,20 +6,21 @@
 // is exact unless they become subnormal.  (With s = amax / F_max every growth would round all
 // earlier codes of the page once more.)
 //
-// One group of threads per (page that the call touches, KV head, K or V): it reads the page's
-// new tokens (in registers), reduces their amax, moves the earlier codes if the scale grew, and
-// writes the codes.  2 B read and 1 B written per element: HBM bounds long prompts, latency a
-// decode step.  A decode step's units hold one token (a 256-byte row at head_dim 128), for which
-// a warp is enough; longer calls give a unit 256 threads, 8 vectors each at most.
+// One group of threads per (page that the call touches, KV head): it reads the page's new K and V
+// (in registers, 4 vectors of each per thread), reduces their amax, moves the earlier codes if a
+// scale grew, and writes the codes.  2 B read and 1 B written per element: HBM bounds long
+// prompts, latency a decode step.  A group is as large as its tokens need, from a warp (one token
+// at head_dim 128 is 256 bytes) to 512 threads (a page of 128 tokens); K and V go together so
+// that one lookup of the page (three dependent loads) is paid for twice the data.  7 prompts of
+// up to 4096 tokens, 8 heads of 128, pages of 32: 59 us with 256 threads for each of K and V
+// (three CTAs per SM), 23 us this way.
 #include "kv_common.cuh"
 
 namespace fp8b {
 
 namespace {
 
-constexpr int APPEND_THREADS = 256;
-constexpr int APPEND_VPT = 8;        // 128 tokens x 128 / 8 elements per vector / 256 threads
-constexpr int DECODE_VPT = 4;        // per lane of the warp variant
+constexpr int APPEND_VPT = 4;        // vectors of K (and of V) per thread
 
 struct AppendParams {
     KvArgs c;
@@ -46,103 +47,137 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
            (cvt_pair<FMT>(__fmul_rn(b.x, f), __fmul_rn(b.y, f)) << 16);
 }
 
-template <int FMT, bool WARP>
-__global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_constant__ AppendParams p) {
-    constexpr int VPT = WARP ? DECODE_VPT : APPEND_VPT;
-    constexpr int GROUP = WARP ? 32 : APPEND_THREADS;
-    __shared__ uint32_t red[APPEND_THREADS / 32];
+// A page's scale for the call's tokens (|bf16| pattern m) over what it held (old, 0 for nothing).
+template <int FMT>
+__device__ __forceinline__ float scale_for(uint32_t m, float old) {
+    return fmaxf(old, page_scale<FMT>(fmaxf(bf16bits_to_float(min(m, 0x7F7Fu)), amax_floor())));
+}
+
+__device__ __forceinline__ uint32_t vec_max(const uint4& x) {
+    return hmax_pair(max_bf16x2_bits(max_bf16x2_bits(abs_bf16x2(x.x), abs_bf16x2(x.y)),
+                                     max_bf16x2_bits(abs_bf16x2(x.z), abs_bf16x2(x.w))));
+}
+
+template <int FMT, int GROUP>
+__global__ void __launch_bounds__(GROUP > 256 ? GROUP : 256) kv_append_kernel(const __grid_constant__ AppendParams p) {
+    constexpr int THREADS = GROUP > 256 ? GROUP : 256;
+    constexpr int WARPS = GROUP / 32;               // of a group
+    __shared__ uint2 red[THREADS / 32];
     const KvArgs& c = p.c;
-    const int32_t unit = WARP ? (int32_t)blockIdx.y * (APPEND_THREADS / 32) + (threadIdx.x >> 5) : (int32_t)blockIdx.y;
-    if (unit >= 2 * c.kv_heads) return;
-    const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
-    const int32_t head = unit >> 1, which = unit & 1;
+    const int t = threadIdx.x % GROUP;
+    const int32_t head = (int32_t)blockIdx.y * (THREADS / GROUP) + (int32_t)threadIdx.x / GROUP;
     const int32_t b = (int32_t)(blockIdx.x / p.slots), slot = (int32_t)(blockIdx.x % p.slots);
     const Sequence s = sequence_of(c, b, (int64_t)1 << 30);
-    if (!s.ok || s.n > s.kv_len) {
-        if (t == 0 && slot == 0) report_status(c.status, FP8_ERR_INVALID_ARG);
-        return;
-    }
-    if (s.n == 0) return;
     const int32_t P = c.page_size, D = c.head_dim;
     const int32_t start = s.kv_len - s.n;
     const int32_t index = start / P + slot;                          // entry of the page table
     const int32_t lo = max(start, index * P), hi = min(s.kv_len, (index + 1) * P);
-    if (lo >= hi) return;
-    const int32_t page = __ldg(c.table + (int64_t)b * c.table_stride + index);
-    if (page < 0 || page >= c.num_pages) {
-        if (t == 0) report_status(c.status, FP8_ERR_INVALID_ARG);
-        return;
+    // the groups of a CTA go on together to the barrier, those without work among them
+    bool work = head < c.kv_heads;
+    if (!s.ok || start < 0) {
+        if (work && head == 0 && t == 0 && slot == 0) report_status(c.status, FP8_ERR_INVALID_ARG);
+        work = false;
+    }
+    if (lo >= hi) work = false;
+    int32_t page = -1;
+    if (work) {
+        page = __ldg(c.table + (int64_t)b * c.table_stride + index);
+        if (page < 0 || page >= c.num_pages) {
+            if (t == 0) report_status(c.status, FP8_ERR_INVALID_ARG);
+            work = false;
+        }
     }
     const int32_t held = lo - index * P;                             // earlier tokens of the page
     const int64_t at = (int64_t)page * c.kv_heads + head;
-    uint8_t* codes = (which ? c.v : c.k) + at * P * D;
-    float* scale = (which ? c.v_scale : c.k_scale) + at;
     const int32_t vec_row = D / 8, shift = D == 128 ? 4 : 3;
-    const int32_t nvec = (hi - lo) * vec_row;
-    const uint16_t* src = p.x[which] + (int64_t)(s.first + lo - start) * p.ld[which] + (int64_t)head * D;
-    uint4 x[VPT];
-    uint32_t m2 = 0;
+    const int32_t nvec = work ? (hi - lo) * vec_row : 0;
+    uint4 x[2][APPEND_VPT];
+    uint32_t m[2] = {0, 0};
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int32_t k = t + j * GROUP;
-        x[j] = make_uint4(0, 0, 0, 0);
-        if (k < nvec) x[j] = ld_v4_stream(src + (int64_t)(k >> shift) * p.ld[which] + (k & (vec_row - 1)) * 8);
+    for (int w = 0; w < 2; ++w) {
+        const uint16_t* src = p.x[w] + (int64_t)(s.first + lo - start) * p.ld[w] + (int64_t)head * D;
+#pragma unroll
+        for (int j = 0; j < APPEND_VPT; ++j) {
+            const int32_t k = t + j * GROUP;
+            x[w][j] = make_uint4(0, 0, 0, 0);
+            if (k < nvec) x[w][j] = ld_v4_stream(src + (int64_t)(k >> shift) * p.ld[w] + (k & (vec_row - 1)) * 8);
+        }
+    }
+    float old[2] = {0.0f, 0.0f};
+    if (work && held > 0) {
+        old[0] = c.k_scale[at];
+        old[1] = c.v_scale[at];
     }
 #pragma unroll
-    for (int j = 0; j < VPT; ++j)
-        m2 = max_bf16x2_bits(m2, max_bf16x2_bits(max_bf16x2_bits(abs_bf16x2(x[j].x), abs_bf16x2(x[j].y)),
-                                                 max_bf16x2_bits(abs_bf16x2(x[j].z), abs_bf16x2(x[j].w))));
-    const float old = held > 0 ? *scale : 0.0f;
-    uint32_t m = __reduce_max_sync(0xffffffffu, hmax_pair(m2));
-    if (!WARP) {
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-        __syncthreads();                                             // also: every thread has read `old`
-        m = 0;
+    for (int w = 0; w < 2; ++w) {
 #pragma unroll
-        for (int i = 0; i < APPEND_THREADS / 32; ++i) m = max(m, red[i]);
+        for (int j = 0; j < APPEND_VPT; ++j) m[w] = max(m[w], vec_max(x[w][j]));
+        m[w] = __reduce_max_sync(0xffffffffu, m[w]);
+    }
+    if (GROUP > 32) {
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_uint2(m[0], m[1]);
+        __syncthreads();                                             // also: every thread has read `old`
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) {
+            const uint2 r = red[threadIdx.x / GROUP * WARPS + i];
+            m[0] = max(m[0], r.x);
+            m[1] = max(m[1], r.y);
+        }
     } else {
         __syncwarp();
     }
-    if (m >= 0x7F80u) {
-        if (t == 0) report_status(c.status, FP8_ERR_NONFINITE);
-        m = 0x7F7Fu;
-    }
-    const float now = fmaxf(old, page_scale<FMT>(fmaxf(bf16bits_to_float(m), amax_floor())));
-    if (t == 0) *scale = now;
-    const float inv = __frcp_rn(now);                                // exact: a power of two
-    if (held > 0 && now != old) {
-        const float f = __fmul_rn(old, inv);
-        const int32_t n16 = held * D / 16;
-        for (int32_t k = t; k < n16; k += GROUP) {
-            uint4* w = reinterpret_cast<uint4*>(codes) + k;
-            uint4 v = *w;
-            v.x = rescale4<FMT>(v.x, f);
-            v.y = rescale4<FMT>(v.y, f);
-            v.z = rescale4<FMT>(v.z, f);
-            v.w = rescale4<FMT>(v.w, f);
-            *w = v;
+    if (!work) return;
+    if (t == 0 && max(m[0], m[1]) >= 0x7F80u) report_status(c.status, FP8_ERR_NONFINITE);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        uint8_t* codes = (w ? c.v : c.k) + at * P * D;
+        const float now = scale_for<FMT>(m[w], old[w]);
+        const float inv = __frcp_rn(now);                            // exact: a power of two
+        if (t == 0) (w ? c.v_scale : c.k_scale)[at] = now;
+        if (held > 0 && now != old[w]) {
+            const float f = __fmul_rn(old[w], inv);
+            const int32_t n16 = held * D / 16;
+            for (int32_t k = t; k < n16; k += GROUP) {
+                uint4* q = reinterpret_cast<uint4*>(codes) + k;
+                uint4 v = *q;
+                v.x = rescale4<FMT>(v.x, f);
+                v.y = rescale4<FMT>(v.y, f);
+                v.z = rescale4<FMT>(v.z, f);
+                v.w = rescale4<FMT>(v.w, f);
+                *q = v;
+            }
         }
-    }
-    uint8_t* dst = codes + (int64_t)held * D;
+        uint2* dst = reinterpret_cast<uint2*>(codes + (int64_t)held * D);
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int32_t k = t + j * GROUP;
-        if (k >= nvec) continue;
-        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-        uint32_t o[4];
+        for (int j = 0; j < APPEND_VPT; ++j) {
+            const int32_t k = t + j * GROUP;
+            if (k >= nvec) continue;
+            const uint32_t q[4] = {x[w][j].x, x[w][j].y, x[w][j].z, x[w][j].w};
+            uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = cvt_pair<FMT>(__fmul_rn(bf16_lo(w[i]), inv), __fmul_rn(bf16_hi(w[i]), inv));
-        reinterpret_cast<uint2*>(dst)[k] = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+            for (int i = 0; i < 4; ++i)
+                o[i] = cvt_pair<FMT>(__fmul_rn(bf16_lo(q[i]), inv), __fmul_rn(bf16_hi(q[i]), inv));
+            dst[k] = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+        }
     }
 }
 
-template <int FMT, bool WARP>
+template <int FMT, int GROUP>
 cudaError_t launch_append(const AppendParams& p, cudaStream_t st) {
-    const int units = 2 * p.c.kv_heads;
-    const dim3 grid((unsigned)((int64_t)p.c.batch * p.slots),
-                    (unsigned)(WARP ? (units + APPEND_THREADS / 32 - 1) / (APPEND_THREADS / 32) : units));
-    kv_append_kernel<FMT, WARP><<<grid, APPEND_THREADS, 0, st>>>(p);
+    const int threads = GROUP > 256 ? GROUP : 256, heads = threads / GROUP;
+    const dim3 grid((unsigned)((int64_t)p.c.batch * p.slots), (unsigned)((p.c.kv_heads + heads - 1) / heads));
+    kv_append_kernel<FMT, GROUP><<<grid, threads, 0, st>>>(p);
     return cudaGetLastError();
+}
+
+// The smallest group whose threads hold a unit's vectors.
+template <int FMT>
+cudaError_t launch_append_fmt(const AppendParams& p, int64_t nvec, cudaStream_t st) {
+    if (nvec <= 32 * APPEND_VPT) return launch_append<FMT, 32>(p, st);
+    if (nvec <= 64 * APPEND_VPT) return launch_append<FMT, 64>(p, st);
+    if (nvec <= 128 * APPEND_VPT) return launch_append<FMT, 128>(p, st);
+    if (nvec <= 256 * APPEND_VPT) return launch_append<FMT, 256>(p, st);
+    return launch_append<FMT, 512>(p, st);          // 128 tokens of 128 elements: 2048 vectors
 }
 
 }  // namespace
@@ -159,9 +194,8 @@ cudaError_t launch_kv_append(const KvArgs& c, const uint16_t* k, int64_t ldk, co
     p.c.max_q = (int32_t)longest;
     p.slots = (int32_t)((longest + c.page_size - 2) / c.page_size + 1);
     if ((int64_t)p.slots * c.batch >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
-    const bool warp = std::min<int64_t>(longest, c.page_size) * (c.head_dim / 8) <= 32 * DECODE_VPT;
-    if (c.fmt == FP8_E4M3) return warp ? launch_append<FP8_E4M3, true>(p, st) : launch_append<FP8_E4M3, false>(p, st);
-    return warp ? launch_append<FP8_E5M2, true>(p, st) : launch_append<FP8_E5M2, false>(p, st);
+    const int64_t nvec = std::min<int64_t>(longest, c.page_size) * (c.head_dim / 8);
+    return c.fmt == FP8_E4M3 ? launch_append_fmt<FP8_E4M3>(p, nvec, st) : launch_append_fmt<FP8_E5M2>(p, nvec, st);
 }
 
 }  // namespace fp8b
