@@ -46,6 +46,22 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+// wait_bounded, but under a short limit (the failure-path tests) no test suspends the thread: these
+// kernels' waits are short, and a test that suspends outlasts them.
+__device__ __forceinline__ bool wait_limited(uint64_t* bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* status,
+                                             uint64_t limit_ns) {
+    if (limit_ns >= 1000000ull) return wait_bounded(bar, parity, abort_flag, status, limit_ns);
+    const uint64_t t0 = ptx::globaltimer();
+    while (!ptx::mbar_test_wait(bar, parity)) {
+        if (*abort_flag) return false;
+        if (ptx::globaltimer() - t0 > limit_ns) {
+            *abort_flag = 1;
+            report_status(status, FP8_ERR_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
 __device__ __forceinline__ uint16_t* out_row(const AttnParams& p, const Sequence& s, int32_t h, int32_t row, int32_t D) {
     return p.out + (int64_t)(s.first + row / p.group) * p.ldo + (int64_t)(h * p.group + row % p.group) * D;
 }

@@ -58,7 +58,7 @@ __device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t smem_addr, uint
 
 // A wait that all lanes of a warp leave with the same outcome.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars* bars, const AttnParams& p) {
-    const bool ok = wait_bounded(bar, parity, &bars->abort_flag, p.c.status, p.wait_ns);
+    const bool ok = wait_limited(bar, parity, &bars->abort_flag, p.c.status, p.wait_ns);
     return __all_sync(0xffffffffu, ok);
 }
 
