@@ -147,6 +147,12 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _on_current_device(t):
+    """The library works on the current device; a tensor elsewhere is refused here."""
+    if not t.is_cuda or (t.get_device() != torch._C._cuda_getDevice()):
+        raise ValueError("the tensors must be on the current CUDA device")
+
+
 def _nbytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
@@ -337,6 +343,7 @@ def fp8_scaled_gemm_act(a, a_scale, a_mode, fmt_a, b, b_scale, b_mode, fmt_b, y,
     N = b.shape[0]
     ldy = 0 if y is None else (y.stride(0) if y.shape[0] > 1 else y.shape[1])
     epi = _epilogue_act(M, N, bias, activation, residual, amax, yq, yq_scale, yq_fmt)
+    _on_current_device(a)
     rc = _lib.fp8_scaled_gemm_act(_ptr(a), _ptr(a_scale), a_mode, fmt_a, _ptr(b), _ptr(b_scale), b_mode, fmt_b,
                                   M, N, K, _ptr(y), ldy, ctypes.byref(epi), _ptr(dev_status), _ptr(workspace),
                                   _nbytes(workspace), _stream(stream))
@@ -354,6 +361,7 @@ def fp8_linear_forward_act(x, x_fmt, x_mode, w, w_scale, w_mode, w_fmt, y, works
     ldx = x.stride(0) if M > 1 else K
     ldy = 0 if y is None else (y.stride(0) if y.shape[0] > 1 else y.shape[1])
     epi = _epilogue_act(M, N, bias, activation, residual, amax, yq, yq_scale, yq_fmt)
+    _on_current_device(x)
     rc = _lib.fp8_linear_forward_act(_ptr(x), M, K, ldx, x_fmt, x_mode,
                                      ctypes.byref(hist.c) if hist is not None else None, _ptr(w), _ptr(w_scale),
                                      w_mode, w_fmt, N, _ptr(y), ldy, ctypes.byref(epi), _ptr(dev_status),
@@ -393,6 +401,7 @@ def fp8_rmsnorm_quantize(x, weight, eps, fmt, mode, q, scale, *, residual=None, 
         raise TypeError("y must be dense bf16 [rows, cols]")
     if amax is not None and amax.dtype is not torch.float32:
         raise TypeError("amax must be fp32")
+    _on_current_device(x)
     rc = _lib.fp8_rmsnorm_quantize(_ptr(x), rows, cols, ldx, _ptr(residual), ldr, _ptr(sum_out), lds, _ptr(weight),
                                    float(eps), fmt, mode, _ptr(amax), _ptr(q), _ptr(scale), _ptr(y), _ptr(dev_status),
                                    _stream(stream))
@@ -431,7 +440,7 @@ class KVCache:
         batch, pages = shape
         if kv_lens.dtype is not torch.int32 or kv_lens.shape != (batch,) or not kv_lens.is_contiguous():
             raise TypeError("kv_lens must be int32 [batch]")
-        c = self.c
+        c = fp8_kv_cache_t.from_buffer_copy(self.c)      # the call's own: calls of two threads may overlap
         c.page_table_dev, c.max_pages = page_table.data_ptr(), pages
         c.table_stride = stride[0] if batch > 1 and pages else pages
         c.kv_lens_dev, c.batch = kv_lens.data_ptr(), batch
@@ -463,8 +472,10 @@ def fp8_kv_append(k, v, cache: KVCache, page_table, kv_lens, *, cu_q=None, max_q
     if k.shape[0] != v.shape[0]:
         raise TypeError("k and v must have as many tokens")
     c = cache.view(page_table, kv_lens)
-    _check(_lib.fp8_kv_append(ctypes.byref(c), _ptr(k), ldk, _ptr(v), ldv, k.shape[0], _cu_q(cu_q, c.batch), max_q_len,
-                              _ptr(dev_status), _stream(stream)), "fp8_kv_append")
+    cu = _cu_q(cu_q, c.batch)
+    _on_current_device(k)
+    _check(_lib.fp8_kv_append(ctypes.byref(c), _ptr(k), ldk, _ptr(v), ldv, k.shape[0], cu, max_q_len, _ptr(dev_status),
+                              _stream(stream)), "fp8_kv_append")
 
 
 def fp8_kv_attention_workspace_size(batch: int, q_heads: int, kv_heads: int, head_dim: int, max_q_len: int,
@@ -488,8 +499,10 @@ def fp8_kv_attention(q, cache: KVCache, page_table, kv_lens, out, *, max_kv_len,
     ldq = _head_rows(q, "q", heads, cache.head_dim)
     ldo = _head_rows(out, "out", heads, cache.head_dim)
     c = cache.view(page_table, kv_lens)
+    cu = _cu_q(cu_q, c.batch)
     scale = dim ** -0.5 if softmax_scale is None else float(softmax_scale)
-    _check(_lib.fp8_kv_attention(ctypes.byref(c), _ptr(q), ldq, heads, tokens, _cu_q(cu_q, c.batch), max_q_len,
+    _on_current_device(q)
+    _check(_lib.fp8_kv_attention(ctypes.byref(c), _ptr(q), ldq, heads, tokens, cu, max_q_len,
                                  max_kv_len, scale, _ptr(out), ldo, _ptr(dev_status), _ptr(workspace),
                                  _nbytes(workspace), _stream(stream)), "fp8_kv_attention")
 

@@ -627,8 +627,10 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         ptx::mbar_init(jfree, 1);
         *ring.abort_flag = 0;
         ptx::fence_mbar_init();
-        ptx::prefetch_tmap(&tk);
-        ptx::prefetch_tmap(&tv);
+        if (p.c.num_pages > 0) {              // else there are no maps (and no tokens)
+            ptx::prefetch_tmap(&tk);
+            ptx::prefetch_tmap(&tv);
+        }
     }
     const Range range = find_range<S>(p, start, sums);       // syncs
     if (range.n == 0) {

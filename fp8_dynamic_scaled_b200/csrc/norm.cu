@@ -59,27 +59,24 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v, uint32_t* red) {
     return __reduce_max_sync(0xffffffffu, lane < nw ? red[lane] : 0u);
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
-    f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x);
-    f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
-    f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z);
-    f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
-}
-__device__ __forceinline__ uint4 pack8(const float* f) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ uint4 pack8(const float2* f) {
+    return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                      pack_bf16x2(f[3].x, f[3].y));
 }
 
-// 8 fp32 values -> 8 codes of y / s (r = RN(1/s), one Markstein step, as in quantize.cu; a
-// quotient that overflows, possible with a given amax only, saturates uncorrected).
+// -y for 8 values -> 8 codes of y / s (r = RN(1/s), one Markstein step on -y, which keeps the sign of
+// a zero, as in quantize.cu; a quotient that overflows, possible with a given amax only,
+// saturates uncorrected).
 template <int FMT, bool GUARD>
-__device__ __forceinline__ uint2 encode8(const float* y, float s, float r) {
+__device__ __forceinline__ uint2 encode8(const float2* ny, float s, float r) {
     uint32_t c[4];
+    const float2 nr = make_float2(-r, -r), s2 = make_float2(s, s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 ny = make_float2(-y[2 * i], -y[2 * i + 1]), nr = make_float2(-r, -r);
-        const float2 q = mul2_rn(ny, nr);
-        float2 t = fma2_rn(fma2_rn(q, make_float2(s, s), ny), nr, q);
+        const float2 q = mul2_rn(ny[i], nr);
+        float2 t = fma2_rn(fma2_rn(q, s2, ny[i]), nr, q);
         if (GUARD) {
             if (!(fabsf(q.x) <= 3.402823466e38f)) t.x = q.x;
             if (!(fabsf(q.y) <= 3.402823466e38f)) t.y = q.y;
@@ -87,6 +84,13 @@ __device__ __forceinline__ uint2 encode8(const float* y, float s, float r) {
         c[i] = cvt_pair<FMT>(t.x, t.y);
     }
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// max(|a|, |b|), NaN if either is.
+__device__ __forceinline__ float max_abs_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return d;
 }
 
 // MODE: fp8_scaling_t.  VPT: 16-byte vectors of a row per thread.  WARP: a warp per row
@@ -99,7 +103,8 @@ __global__ void __launch_bounds__(WARP ? 32 * WARP_ROWS : 1024) rmsnorm_quantize
     if (WARP && row >= p.rows) return;
     const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
     const int step = WARP ? 32 : blockDim.x;
-    float h[VPT][NVEC];
+    float2 h[VPT][NVEC / 2];
+    uint4 wv[VPT];
     {
         uint4 xv[VPT], rv[VPT];
 #pragma unroll
@@ -116,23 +121,27 @@ __global__ void __launch_bounds__(WARP ? 32 * WARP_ROWS : 1024) rmsnorm_quantize
                 if (k < p.nvec) rv[j] = ld_v4_stream(p.res + row * p.ldr + k * NVEC);
             }
         }
+        // the weight comes from L2, ahead of the reduction that it follows
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            unpack8(xv[j], h[j]);
-            if (p.res) {
-                float r[NVEC];
-                unpack8(rv[j], r);
-#pragma unroll
-                for (int i = 0; i < NVEC; ++i) h[j][i] = __fadd_rn(h[j][i], r[i]);
-            }
+            const int k = t + j * step;
+            wv[j] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+            if (p.weight && k < p.nvec) wv[j] = __ldg(reinterpret_cast<const uint4*>(p.weight + k * NVEC));
         }
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int i = 0; i < NVEC / 2; ++i) {
+                h[j][i] = unpack2(word(xv[j], i));
+                if (p.res) h[j][i] = add2_rn(h[j][i], unpack2(word(rv[j], i)));
+            }
     }
-    float ss = 0.0f;
+    float2 ss2 = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
 #pragma unroll
-        for (int i = 0; i < NVEC; ++i) ss = fmaf(h[j][i], h[j][i], ss);
-    ss = group_sum<WARP>(ss, red_sum[0]);
+        for (int i = 0; i < NVEC / 2; ++i) ss2 = fma2_rn(h[j][i], h[j][i], ss2);
+    const float ss = group_sum<WARP>(ss2.x + ss2.y, red_sum[0]);
     if (p.sum) {
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
@@ -142,38 +151,36 @@ __global__ void __launch_bounds__(WARP ? 32 * WARP_ROWS : 1024) rmsnorm_quantize
     }
     // 1 / sqrt(mean + eps); squares that leave the fp32 range (|h| above 1e19) are summed
     // again at 2^-80 of their size.  The branch is the same for the whole row.
-    float rstd, pre = 1.0f;
+    float rstd;
     if (ss <= 3.402823466e38f) {
         rstd = __frsqrt_rn(fmaf(ss, p.inv_cols, p.eps));
     } else {
-        pre = 8.271806125530277e-25f;                 // 2^-80
+        const float pre = 8.271806125530277e-25f;     // 2^-80
         float s2 = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
 #pragma unroll
-            for (int i = 0; i < NVEC; ++i) s2 = fmaf(h[j][i] * pre, h[j][i] * pre, s2);
-        rstd = __frsqrt_rn(group_sum<WARP>(s2, red_sum[1]) * p.inv_cols);   // eps is far below
+            for (int i = 0; i < NVEC / 2; ++i) {
+                s2 = fmaf(h[j][i].x * pre, h[j][i].x * pre, s2);
+                s2 = fmaf(h[j][i].y * pre, h[j][i].y * pre, s2);
+            }
+        // eps is far below; the product may be subnormal, with 21 bits at least
+        rstd = pre * __frsqrt_rn(group_sum<WARP>(s2, red_sum[1]) * p.inv_cols);
     }
+    // h becomes -y
+    float m[VPT];
+    float top = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int k = t + j * step;
-        float w[NVEC];
-        uint4 wv = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-        if (p.weight && k < p.nvec) wv = __ldg(reinterpret_cast<const uint4*>(p.weight + k * NVEC));
-        unpack8(wv, w);
+        m[j] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NVEC; ++i) h[j][i] = h[j][i] * pre * rstd * w[i];
+        for (int i = 0; i < NVEC / 2; ++i) {
+            h[j][i] = mul2_rn(mul2_rn(h[j][i], make_float2(-rstd, -rstd)), unpack2(word(wv[j], i)));
+            m[j] = max_abs_nan(m[j], max_abs_nan(h[j][i].x, h[j][i].y));
+        }
+        top = max_abs_nan(top, m[j]);
     }
-    // from here h holds y
-    uint32_t m[VPT];
-    uint32_t all = 0;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        m[j] = 0;
-#pragma unroll
-        for (int i = 0; i < NVEC; ++i) m[j] = max(m[j], __float_as_uint(h[j][i]) & 0x7FFFFFFFu);
-        all = max(all, m[j]);
-    }
+    const uint32_t all = __float_as_uint(top) & 0x7FFFFFFFu;     // patterns order like the values, NaN above
     float s = 1.0f, r = 1.0f;
     if (MODE == FP8_SCALE_ROW) {
         uint32_t a = group_max<WARP>(all, red_max);
@@ -200,7 +207,7 @@ __global__ void __launch_bounds__(WARP ? 32 * WARP_ROWS : 1024) rmsnorm_quantize
         const int k = t + j * step;
         if (MODE == FP8_SCALE_BLOCK_1x128 || MODE == FP8_SCALE_MX32) {
             // a block is 16 (4) vectors, held by as many neighbouring lanes
-            uint32_t a = m[j];
+            uint32_t a = __float_as_uint(m[j]) & 0x7FFFFFFFu;
 #pragma unroll
             for (int o = MODE == FP8_SCALE_MX32 ? 2 : 8; o > 0; o >>= 1)
                 a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
@@ -224,13 +231,23 @@ __global__ void __launch_bounds__(WARP ? 32 * WARP_ROWS : 1024) rmsnorm_quantize
         if (MODE == FP8_SCALE_MX32) {
             uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = cvt_pair<FMT>(__fmul_rn(h[j][2 * i], r), __fmul_rn(h[j][2 * i + 1], r));
+            for (int i = 0; i < 4; ++i) {
+                const float2 q = mul2_rn(h[j][i], make_float2(-r, -r));
+                w[i] = cvt_pair<FMT>(q.x, q.y);
+            }
             c = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
         } else {
             c = encode8<FMT, MODE == FP8_SCALE_TENSOR>(h[j], s, r);
         }
         *reinterpret_cast<uint2*>(p.q + row * p.cols + k * NVEC) = c;
-        if (p.y) st_v4_stream(p.y + row * p.cols + k * NVEC, pack8(h[j]));
+        if (p.y) {
+            uint4 y = pack8(h[j]);
+            y.x ^= 0x80008000u;
+            y.y ^= 0x80008000u;
+            y.z ^= 0x80008000u;
+            y.w ^= 0x80008000u;
+            st_v4_stream(p.y + row * p.cols + k * NVEC, y);
+        }
     }
 }
 

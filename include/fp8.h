@@ -476,7 +476,8 @@ typedef struct {
  *   tokens        rows of k_dev / v_dev (== batch when cu_q_dev is NULL).
  *   dev_status    nullable; FP8_ERR_NONFINITE for a NaN/Inf element (that page and head are
  *                 then unspecified), FP8_ERR_INVALID_ARG as above.
- * No two sequences of a call may append to one page (pages that sequences share are full).
+ * No two sequences of a call may append to one page (pages that sequences share are full), and a
+ * page that tokens are added to carries scales that this call wrote (powers of two).
  * No workspace.  Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA.
  */
 FP8_API int32_t fp8_kv_append(const fp8_kv_cache_t* cache, const void* k_dev, int64_t ldk, const void* v_dev,
@@ -492,14 +493,15 @@ FP8_API int32_t fp8_kv_append(const fp8_kv_cache_t* cache, const void* k_dev, in
  * in fp16 (codes exactly; a query row after a power-of-two normalisation; the weights p),
  * out is rounded once to bf16.  A query that sees no token (kv_len 0) gives zeros.
  *   q_dev, out_dev  bf16 [tokens][q_heads][head_dim], token strides ldq / ldo (% 8 == 0,
- *                   >= q_heads head_dim), 16-byte aligned.
+ *                   >= q_heads head_dim), 16-byte aligned.  q is finite.
  *   q_heads         a multiple of kv_heads.
  *   max_kv_len      bounds every kv_lens[b].  It and max_q_len size the launch.
  *   softmax_scale   finite.
  *   workspace       fp8_kv_attention_workspace_size bytes, 16-byte aligned, needs no
  *                   initialisation; calls that share one must not overlap on the GPU.
- * The result does not depend on the batch's other sequences' contents, and is the same from
- * run to run for the same sizes.  Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE,
+ * The result does not depend on the batch's other sequences' contents (their lengths decide where
+ * the work is split, and with it the order of a few fp32 sums), and is the same from run to
+ * run for the same lengths.  Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE,
  * WORKSPACE, CUDA.
  */
 FP8_API size_t fp8_kv_attention_workspace_size(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
