@@ -141,3 +141,19 @@ def test_kv_binding_type_checks():
         b.fp8_kv_append(x, x, cache, table, lens, cu_q=torch.zeros(2, dtype=torch.int32))
     with pytest.raises(TypeError):
         b.fp8_kv_attention(x, cache, table, lens, x[:1], max_kv_len=16)
+
+
+def test_tensors_off_the_current_device_are_refused():
+    """Well-formed calls with host tensors: refused in the binding, before the library sees a pointer."""
+    cache = b.KVCache.empty(4, 2, 16, 64, device="cpu")
+    table, lens = torch.zeros((2, 3), dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    kv = torch.empty((2, 2, 64), dtype=torch.bfloat16)
+    x, q, s = torch.empty((4, 64), dtype=torch.bfloat16), torch.empty((4, 64), dtype=torch.uint8), torch.empty(4)
+    w, y = torch.empty((8, 64), dtype=torch.uint8), torch.empty((4, 8), dtype=torch.bfloat16)
+    for call in (lambda: b.fp8_kv_append(kv, kv, cache, table, lens),
+                 lambda: b.fp8_kv_attention(kv, cache, table, lens, kv.clone(), max_kv_len=16),
+                 lambda: b.fp8_rmsnorm_quantize(x, None, 1e-5, 0, 1, q, s),
+                 lambda: b.fp8_scaled_gemm_act(q, s, 1, 0, w, s, 1, 0, y),
+                 lambda: b.fp8_linear_forward_act(x, 0, 1, w, s, 1, 0, y, q)):
+        with pytest.raises(ValueError):
+            call()
