@@ -528,15 +528,22 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 //   warp 0   TMA producer (both CTAs), completion on the local full[] barrier
 //   warp 1   TMEM allocator (both CTAs, cta_group::2); MMA issuer (leader only)
 //   warp 2   relay (both CTAs): local full[] -> one arrival on the leader's ready[]
-//   warps 3-6 epilogue (both CTAs) on the CTA's own 128 accumulator rows; they
+//   warps 3-6 (3-10 with EPI_ACT) epilogue (both CTAs) on the CTA's own 128 accumulator rows; they
 //            release an accumulator with one arrival each on the leader's tempty[]
 // The leader's commits arrive on empty[] / tfull[] in both CTAs (multicast commit).
 constexpr int P_BM = 256;                                  // rows per CTA-pair tile
 constexpr int P_STAGES = 6;
 constexpr uint32_t P_HALF_BYTES = 128 * BK;                // 16 KB: one CTA's half of A or B
+template <int EXT>
 struct PairSmem {
-    static constexpr int NT = 7 * 32;
-    static constexpr int EPI_WARPS = 4, FIRST_EPI_WARP = 3, STAGE_BUFS = 2;
+    // with an activation or a residual the epilogue outlasts the products of a short K: two warps
+    // share each lane quarter then, half of the columns each (2048 x 8192 outputs, K = 1024: SiLU
+    // 55 -> 44 us, bias, GELU and residual 78 -> 59; 4096 x 28672, K = 8192, SiLU and FP8 output, where
+    // the products hide it: 713 -> 719)
+    static constexpr int EPI_WARPS = EXT == EPI_ACT ? 8 : 4;
+    static constexpr int FIRST_EPI_WARP = 3, STAGE_BUFS = 2;
+    static constexpr int NT = (FIRST_EPI_WARP + EPI_WARPS) * 32;
+    static constexpr int CHUNKS = BN / 32 / (EPI_WARPS / 4);   // of a warp, per tile
     static constexpr uint32_t A_OFF = 0;
     static constexpr uint32_t B_OFF = A_OFF + P_STAGES * P_HALF_BYTES;
     static constexpr uint32_t Y_OFF = B_OFF + P_STAGES * P_HALF_BYTES;
@@ -550,10 +557,10 @@ struct PairSmem {
 };
 
 template <int EXT>
-__global__ void __launch_bounds__(PairSmem::NT, 1)
+__global__ void __launch_bounds__(PairSmem<EXT>::NT, 1)
 fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmY, const GemmParams p) {
-    using S = PairSmem;
+    using S = PairSmem<EXT>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem + S::A_OFF;
@@ -679,6 +686,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         pdl_wait();                           // the scales may come from the kernel just before
         const int ew = warp - S::FIRST_EPI_WARP;
         const int quarter = warp & 3;
+        const int c0 = (ew >> 2) * S::CHUNKS;                // this warp's first 32 columns of a tile
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         uint8_t* ybuf = sY + ew * S::STAGE_BUFS * 2048;
         uint32_t acc_it = 0, store_it = 0;
@@ -693,16 +701,16 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             const uint32_t buf = acc_it & 1u, use = acc_it >> 1;
             ResidualChunk rc;
             uint32_t res[16];
-            if (EXT == EPI_ACT && p.res) rc.load(p, nb * BN, y_row0, lane);      // see fp8_gemm_kernel
+            if (EXT == EPI_ACT && p.res) rc.load(p, nb * BN + c0 * 32, y_row0, lane);   // see fp8_gemm_kernel
             if (!wait_bounded(&tfull[buf], use & 1u, abort_flag, p.status, p.wait_ns)) { ok = false; break; }
             ptx::tc_fence_after();
             const float sx = row < p.M ? __ldg(p.sa + (int64_t)row * p.sa_stride) : 0.0f;
 #pragma unroll 1
-            for (int c = 0; c < BN / 32; ++c) {
+            for (int c = c0; c < c0 + S::CHUNKS; ++c) {
                 uint32_t r[32];
                 ptx::tmem_ld_32x32b_x32(tmem_base + lane_base + buf * BN + c * 32, r);
                 ptx::tmem_ld_wait();
-                if (c == BN / 32 - 1) {
+                if (c == c0 + S::CHUNKS - 1) {
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive_cluster(&tempty[buf], 0);
@@ -716,7 +724,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 }
                 if (EXT == EPI_ACT && p.res) {
                     rc.turn(b, lane, res);
-                    if (c + 1 < BN / 32) rc.load(p, n0 + 32, y_row0, lane);
+                    if (c + 1 < c0 + S::CHUNKS) rc.load(p, n0 + 32, y_row0, lane);
                 }
                 rowscale_chunk<EXT>(p, es, r, res, sx, n0, p.N, row, w, b);
                 if (n0 < p.N && (!EXT || p.write_y)) {
@@ -810,12 +818,12 @@ static cudaError_t launch_pair(const GemmArgs& g, GemmParams p, cudaStream_t st)
     int max_clusters = ds >= 0 ? max_clusters_of[ds] : 0;
     if (max_clusters == 0) {
         cudaError_t e = cudaFuncSetAttribute(fp8_gemm_pair_kernel<EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)PairSmem::ALLOC);
+                                             (int)PairSmem<EXT>::ALLOC);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t q = {};
         q.gridDim = dim3(2 * (num_sms() / 2));
-        q.blockDim = dim3(PairSmem::NT);
-        q.dynamicSmemBytes = PairSmem::ALLOC;
+        q.blockDim = dim3(PairSmem<EXT>::NT);
+        q.dynamicSmemBytes = PairSmem<EXT>::ALLOC;
         cudaLaunchAttribute qa[1];
         qa[0].id = cudaLaunchAttributeClusterDimension;
         qa[0].val.clusterDim.x = 2;
@@ -833,8 +841,8 @@ static cudaError_t launch_pair(const GemmArgs& g, GemmParams p, cudaStream_t st)
     const int clusters = std::max(1, std::min(tiles, max_clusters));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * clusters);
-    cfg.blockDim = dim3(PairSmem::NT);
-    cfg.dynamicSmemBytes = PairSmem::ALLOC;
+    cfg.blockDim = dim3(PairSmem<EXT>::NT);
+    cfg.dynamicSmemBytes = PairSmem<EXT>::ALLOC;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
