@@ -15,6 +15,12 @@
 // (its products are then complete: they were issued before the scores' whose barrier the
 // thread has waited for).
 //
+// Measured: three chunks (2048 new tokens of 6001, 587 of 3535, 512 of 4546; 32 / 8 heads of 128)
+// 310 us = 755 TFLOP/s, a step of both tiles in some 4,900 cycles.  The products alone would take
+// 2,048; the chain scores -> weights -> output of each tile bounds it (2,000-2,400 cycles for the
+// weights, 1,400 for a tile's two products, the hand-overs): without the exponentials it is 2 %
+// faster, without the loads 10 %, without either product 5 %.
+//
 // Roles: warp 0 issues the MMAs; warps 4-7 convert; warps 8-11 and 12-15 hold the rows.
 #include "attention_common.cuh"
 

