@@ -8,9 +8,9 @@
 // thread issued before the first use, stays in registers through its two reductions (the
 // sum of squares; the amax, over the row or a 128- or 32-element group of it), and is
 // written once.  The division by the scale is the corrected reciprocal of quantize.cu.
-// Measured: 16384 x 8192 with a residual, 1x128 scales (939 MB) 148 us in a burst = 6.3 TB/s, 151-162
-// sustained (a plain copy of as many bytes, sustained: 151); 1 row of 8192 2.7 us; 1021 x 5152, MX32,
-// 6.1 us.
+// Measured: 16384 x 8192 with a residual, 1x128 scales (939 MB) 148 us in a burst = 6.3 TB/s, 151-168
+// sustained (a plain copy of as many bytes, sustained: 151); 1 row of 8192 2.4 us; 1021 x 5152, MX32,
+// 5.8 us.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -268,6 +268,11 @@ cudaError_t launch_mode(const NormParams& p, cudaStream_t st) {
     if (p.nvec <= 32) return launch_one<FMT, MODE, 1, true>(p, st);
     if (p.nvec <= 64) return launch_one<FMT, MODE, 2, true>(p, st);
     if (p.nvec <= 128) return launch_one<FMT, MODE, 4, true>(p, st);
+    // two vectors per thread for few rows, where a row's latency counts, and for rows of up to 2,048;
+    // four otherwise, where fewer and longer-lived threads leave HBM busier (with 2 and with 4: 1 row of
+    // 8192 2.4 and 2.7 us, 256 rows 3.9 and 4.1, 1021 x 5152 5.8 and 6.3, 16384 x 1088 24 and 29;
+    // 4096 x 8192 46 and 38, 16384 x 8192 156 and 150)
+    if (p.nvec <= 256 || (p.rows <= 1024 && p.nvec <= 2048)) return launch_one<FMT, MODE, 2, false>(p, st);
     return launch_one<FMT, MODE, 4, false>(p, st);     // nvec <= 4096: at most 1024 threads
 }
 

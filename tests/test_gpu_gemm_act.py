@@ -214,3 +214,23 @@ def test_side_stream_and_graph():
         g.replay()
         torch.cuda.synchronize()
         near(y, *expect(ref, bound, None, GELU, res))
+
+
+@pytest.mark.parametrize("am,bm", PAIRS)
+@pytest.mark.parametrize("M,N,ldq", [(9, 131, 131), (70, 270, 275), (290, 33, 40), (290, 515, 515), (257, 1, 3)])
+def test_codes_of_unaligned_rows(M, N, ldq, am, bm):
+    """FP8 output whose rows start at any byte, with and without Y; nothing outside is written."""
+    K = 128
+    (a, sa, b, sb), ref, bound, _ = operands(M, N, K, am, bm, 17)
+    res, s = bf16((M, N), 18), torch.tensor([0.02], device="cuda")
+    y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    for with_y in (True, False):
+        buf = torch.full((M, ldq), 0x55, dtype=torch.uint8, device="cuda")
+        yq = buf[:, ldq - N:]
+        amax = torch.zeros(1, device="cuda")
+        fp8.fp8_scaled_gemm_act(a, sa, am, E4, b, sb, bm, E4, y if with_y else None, activation=SILU, residual=res,
+                                amax=amax, yq=yq, yq_scale=s)
+        near(y, *expect(ref, bound, None, SILU, res))
+        assert amax.item() == y.float().abs().max().item()
+        assert torch.equal(yq, (y.float() / s).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8))
+        assert bool((buf[:, :ldq - N] == 0x55).all())
