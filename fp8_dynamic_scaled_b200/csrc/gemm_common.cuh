@@ -150,11 +150,14 @@ __device__ __forceinline__ void stage_row_sw64(uint8_t* buf, int r, const uint32
     }
 }
 
-// Store a 32-row x 32-column bf16 chunk held one row per lane (columns >= n_lim are
-// not written by the plain-store path; the TMA path clips at the tensor edge).
+// Store a 32-row x 32-column bf16 chunk held one row per lane; columns >= n_lim are not written.
+// The TMA store clips at the tensor's edge only down to whole 16 bytes (with N = 5 in rows of 16
+// elements it wrote columns 5 to 7 as well), so a chunk that ends inside 16 bytes takes the plain
+// stores; it commits an empty group, since the buffers' reuse counts one group per chunk.
 __device__ __forceinline__ void store_chunk(const CUtensorMap* tmY, uint8_t* buf, const uint32_t (&w)[16],
                                             int32_t x, int32_t y, int lane, const GemmParams& p, int32_t n_lim) {
-    if (p.y_direct) {
+    const bool partial = (n_lim & 7) != 0 && n_lim - x < 32;
+    if (p.y_direct || partial) {
         const int32_t row = y + lane;
         if (p.y_vec && n_lim - x >= 32 && (x & 7) == 0) {
             if (row < p.M) {
@@ -179,6 +182,7 @@ __device__ __forceinline__ void store_chunk(const CUtensorMap* tmY, uint8_t* buf
                         buf + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
         }
         __syncwarp();
+        if (lane == 0 && !p.y_direct) ptx::bulk_commit();
         return;
     }
     stage_row_sw64(buf, lane, w);

@@ -140,6 +140,32 @@ def test_strided_and_unaligned_residual(M):
 
 
 @pytest.mark.parametrize("am,bm", PAIRS)
+@pytest.mark.parametrize("M,N", [(2, 1), (7, 5), (100, 39), (147, 372), (300, 3), (290, 250), (586, 1157)])
+def test_columns_beside_y_are_left(M, N, am, bm):
+    """Rows that start on 16 bytes while the last columns end inside 16 bytes: the neighbours of a
+    column view keep their bits, for the plain GEMM, the older options and these."""
+    K = 256
+    (a, sa, b, sb), ref, bound, _ = operands(M, N, K, am, bm, 11)
+    ld = (N + 7) // 8 * 8 + 8
+    res = bf16((M, N), 4, 4.0)
+    for call in range(4):
+        out = torch.full((M, ld), 7.0, dtype=torch.bfloat16, device="cuda")
+        y = out[:, :N]
+        if call == 0:
+            fp8.fp8_scaled_gemm(a, sa, am, E4, b, sb, bm, E4, y)
+        elif call == 1:
+            fp8.fp8_scaled_gemm_ex(a, sa, am, E4, b, sb, bm, E4, y, bias=bf16(N, 1))
+        elif call == 2:
+            fp8.fp8_scaled_gemm_act(a, sa, am, E4, b, sb, bm, E4, y, activation=SILU, residual=res)
+        else:
+            y.copy_(res)
+            fp8.fp8_scaled_gemm_act(a, sa, am, E4, b, sb, bm, E4, y, residual=y)
+        near(y, *expect(ref, bound, bf16(N, 1) if call == 1 else None, SILU if call == 2 else NONE,
+                        res if call > 1 else None), what=f"call {call}")
+        assert bool((out[:, N:] == 7.0).all()), f"call {call}"
+
+
+@pytest.mark.parametrize("am,bm", PAIRS)
 @pytest.mark.parametrize("M", [9, 70, 290])
 def test_amax_and_fp8_output_follow_y(M, am, bm):
     N, K = 272, 128
