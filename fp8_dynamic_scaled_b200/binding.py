@@ -493,7 +493,7 @@ def kv_attention_workspace(q, cache: KVCache, batch: int, max_q_len: int, max_kv
 
 def fp8_kv_attention(q, cache: KVCache, page_table, kv_lens, out, *, max_kv_len, cu_q=None, max_q_len=1,
                      softmax_scale=None, workspace=None, dev_status=None, stream=None):
-    """Causal attention of q (bf16 [tokens, q_heads, head_dim]) over the cache into out (the same shape);
+    """Causal attention of q (bf16 [tokens, q_heads, head_dim]) over the cache into out (the same shape, not q);
     softmax_scale defaults to head_dim ** -0.5."""
     if q.dim() != 3 or out.shape != q.shape:
         raise TypeError("q and out must be bf16 [tokens, q_heads, head_dim]")

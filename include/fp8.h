@@ -494,7 +494,7 @@ FP8_API int32_t fp8_kv_append(const fp8_kv_cache_t* cache, const void* k_dev, in
  * in fp16 (codes exactly; a query row after a power-of-two normalisation; the weights p),
  * out is rounded once to bf16.  A query that sees no token (kv_len 0) gives zeros.
  *   q_dev, out_dev  bf16 [tokens][q_heads][head_dim], token strides ldq / ldo (% 8 == 0,
- *                   >= q_heads head_dim), 16-byte aligned.  q is finite.
+ *                   >= q_heads head_dim), 16-byte aligned.  q is finite; out does not overlap it.
  *   q_heads         a multiple of kv_heads.
  *   max_kv_len      bounds every kv_lens[b].  It and max_q_len size the launch.
  *   softmax_scale   finite.
