@@ -148,10 +148,11 @@ def _stream(stream):
 
 
 def _on_current_device(*tensors):
-    """The library works on the current device; tensors elsewhere are refused here."""
-    device = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+    """The library works on the current device; tensors elsewhere are refused here.  Given every tensor of a
+    call whose address a kernel gets."""
+    device = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != device):
+        if t is not None and t.get_device() != device:            # -1: a host tensor
             raise ValueError("the tensors must be on the current CUDA device")
 
 
@@ -345,7 +346,7 @@ def fp8_scaled_gemm_act(a, a_scale, a_mode, fmt_a, b, b_scale, b_mode, fmt_b, y,
     N = b.shape[0]
     ldy = 0 if y is None else (y.stride(0) if y.shape[0] > 1 else y.shape[1])
     epi = _epilogue_act(M, N, bias, activation, residual, amax, yq, yq_scale, yq_fmt)
-    _on_current_device(a, b, y, residual)
+    _on_current_device(a, a_scale, b, b_scale, y, bias, residual, amax, yq, yq_scale, dev_status)
     rc = _lib.fp8_scaled_gemm_act(_ptr(a), _ptr(a_scale), a_mode, fmt_a, _ptr(b), _ptr(b_scale), b_mode, fmt_b,
                                   M, N, K, _ptr(y), ldy, ctypes.byref(epi), _ptr(dev_status), _ptr(workspace),
                                   _nbytes(workspace), _stream(stream))
@@ -363,7 +364,9 @@ def fp8_linear_forward_act(x, x_fmt, x_mode, w, w_scale, w_mode, w_fmt, y, works
     ldx = x.stride(0) if M > 1 else K
     ldy = 0 if y is None else (y.stride(0) if y.shape[0] > 1 else y.shape[1])
     epi = _epilogue_act(M, N, bias, activation, residual, amax, yq, yq_scale, yq_fmt)
-    _on_current_device(x, w, y, residual)
+    _on_current_device(x, w, w_scale, y, workspace, bias, residual, amax, yq, yq_scale, dev_status)
+    if hist is not None:
+        _on_current_device(hist.ring, hist.pending, hist.ticket)
     rc = _lib.fp8_linear_forward_act(_ptr(x), M, K, ldx, x_fmt, x_mode,
                                      ctypes.byref(hist.c) if hist is not None else None, _ptr(w), _ptr(w_scale),
                                      w_mode, w_fmt, N, _ptr(y), ldy, ctypes.byref(epi), _ptr(dev_status),
@@ -403,7 +406,7 @@ def fp8_rmsnorm_quantize(x, weight, eps, fmt, mode, q, scale, *, residual=None, 
         raise TypeError("y must be dense bf16 [rows, cols]")
     if amax is not None and amax.dtype is not torch.float32:
         raise TypeError("amax must be fp32")
-    _on_current_device(x, weight, residual, q, scale)
+    _on_current_device(x, weight, residual, sum_out, q, scale, y, amax, dev_status)
     rc = _lib.fp8_rmsnorm_quantize(_ptr(x), rows, cols, ldx, _ptr(residual), ldr, _ptr(sum_out), lds, _ptr(weight),
                                    float(eps), fmt, mode, _ptr(amax), _ptr(q), _ptr(scale), _ptr(y), _ptr(dev_status),
                                    _stream(stream))
@@ -421,6 +424,8 @@ class KVCache:
         for t in (k_scale, v_scale):
             if t.dtype != torch.float32 or t.shape != k.shape[:2] or not t.is_contiguous():
                 raise TypeError("k_scale, v_scale must be dense fp32 [num_pages, kv_heads]")
+        if len({t.get_device() for t in (k, v, k_scale, v_scale)}) != 1:
+            raise ValueError("k, v and their scales must be on one device")
         self.k, self.v, self.k_scale, self.v_scale, self.fmt = k, v, k_scale, v_scale, fmt
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         self.c = fp8_kv_cache_t(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.num_pages,
@@ -475,7 +480,7 @@ def fp8_kv_append(k, v, cache: KVCache, page_table, kv_lens, *, cu_q=None, max_q
         raise TypeError("k and v must have as many tokens")
     c = cache.view(page_table, kv_lens)
     cu = _cu_q(cu_q, c.batch)
-    _on_current_device(k, v, cache.k, page_table, kv_lens, cu_q)
+    _on_current_device(k, v, cache.k, page_table, kv_lens, cu_q, dev_status)    # the cache's tensors share a device
     _check(_lib.fp8_kv_append(ctypes.byref(c), _ptr(k), ldk, _ptr(v), ldv, k.shape[0], cu, max_q_len, _ptr(dev_status),
                               _stream(stream)), "fp8_kv_append")
 
@@ -503,7 +508,7 @@ def fp8_kv_attention(q, cache: KVCache, page_table, kv_lens, out, *, max_kv_len,
     c = cache.view(page_table, kv_lens)
     cu = _cu_q(cu_q, c.batch)
     scale = dim ** -0.5 if softmax_scale is None else float(softmax_scale)
-    _on_current_device(q, out, cache.k, page_table, kv_lens, cu_q)
+    _on_current_device(q, out, cache.k, page_table, kv_lens, cu_q, workspace, dev_status)
     _check(_lib.fp8_kv_attention(ctypes.byref(c), _ptr(q), ldq, heads, tokens, cu, max_q_len,
                                  max_kv_len, scale, _ptr(out), ldo, _ptr(dev_status), _ptr(workspace),
                                  _nbytes(workspace), _stream(stream)), "fp8_kv_attention")
