@@ -9,6 +9,7 @@ module fails loudly when the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -321,6 +322,33 @@ def fp8_linear_forward_ex(x, x_fmt, x_mode, w, w_scale, w_mode, w_fmt, y, worksp
     _check(rc, "fp8_linear_forward_ex")
 
 
+def _check_gemm_act(M, N, K, w, y, bias, amax, yq, yq_scale):
+    """Shapes and types of what the *_act calls take beside their first operand; returns y's row stride."""
+    if w.dim() != 2 or w.shape[1] != K or not w.is_contiguous():
+        raise TypeError(f"the weight must be dense uint8 codes [N, {K}]")
+    ldy = 0
+    for name, t in (("y", y), ("yq", yq)):
+        if t is not None and (t.shape != (M, N) or (N > 1 and t.stride(1) != 1)):
+            raise TypeError(f"{name} must be [{M}, {N}] with unit column stride")
+    if y is not None:
+        ldy = y.stride(0) if M > 1 else N
+    if bias is not None and not bias.is_contiguous():
+        raise TypeError("bias must be dense bf16 [N]")
+    for name, t in (("amax", amax), ("yq_scale", yq_scale)):
+        if t is not None and (t.dtype is not torch.float32 or t.numel() < 1):
+            raise TypeError(f"{name} must be a device fp32")
+    return ldy
+
+
+def _check_scale(name, scale, mode, rows, cols):
+    """A buffer of the mode's scales for [rows, cols] codes (a mode that does not exist is the library's to refuse)."""
+    if scale is not None and FP8_SCALE_TENSOR <= mode <= FP8_SCALE_DELAYED:
+        one_byte = mode == FP8_SCALE_MX32                          # uint8 or float8_e8m0fnu
+        if (scale.element_size() != 1 if one_byte else scale.dtype is not torch.float32) or not scale.is_contiguous() or \
+                scale.numel() < math.prod(scale_shape(mode, rows, cols)):
+            raise TypeError(f"{name} must be a dense buffer of the mode's scales")
+
+
 def _epilogue_act(M, N, bias, activation, residual, amax, yq, yq_scale, yq_fmt):
     epi = fp8_epilogue_act_t()
     base = _epilogue(N, bias, amax, yq, yq_scale, yq_fmt)
@@ -342,11 +370,16 @@ def fp8_scaled_gemm_act(a, a_scale, a_mode, fmt_a, b, b_scale, b_mode, fmt_b, y,
     (bf16 [M, N]) may be y itself; y may be None when yq is given."""
     if a.dtype != torch.uint8 or b.dtype != torch.uint8 or (y is not None and y.dtype != torch.bfloat16):
         raise TypeError("a, b must be uint8 codes and y bf16")
+    if a.dim() != 2 or not a.is_contiguous():
+        raise TypeError("a must be dense uint8 codes [M, K]")
     M, K = a.shape
     N = b.shape[0]
-    ldy = 0 if y is None else (y.stride(0) if y.shape[0] > 1 else y.shape[1])
+    ldy = _check_gemm_act(M, N, K, b, y, bias, amax, yq, yq_scale)
     epi = _epilogue_act(M, N, bias, activation, residual, amax, yq, yq_scale, yq_fmt)
     _on_current_device(a, a_scale, b, b_scale, y, bias, residual, amax, yq, yq_scale, dev_status)
+    if K and N:
+        _check_scale("a_scale", a_scale, a_mode, M, K)
+        _check_scale("b_scale", b_scale, b_mode, N, K)
     rc = _lib.fp8_scaled_gemm_act(_ptr(a), _ptr(a_scale), a_mode, fmt_a, _ptr(b), _ptr(b_scale), b_mode, fmt_b,
                                   M, N, K, _ptr(y), ldy, ctypes.byref(epi), _ptr(dev_status), _ptr(workspace),
                                   _nbytes(workspace), _stream(stream))
@@ -359,14 +392,18 @@ def fp8_linear_forward_act(x, x_fmt, x_mode, w, w_scale, w_mode, w_fmt, y, works
     """fp8_linear_forward with the epilogue of fp8_scaled_gemm_act."""
     if x.dtype != torch.bfloat16 or w.dtype != torch.uint8 or (y is not None and y.dtype != torch.bfloat16):
         raise TypeError("x bf16, w uint8 codes, y bf16")
+    if x.dim() != 2:
+        raise TypeError("x must be a 2-D bf16 tensor with unit column stride")
     M, K = x.shape
     N = w.shape[0]
-    ldx = x.stride(0) if M > 1 else K
-    ldy = 0 if y is None else (y.stride(0) if y.shape[0] > 1 else y.shape[1])
+    ldx = _rows_of(x, "x", M, K)
+    ldy = _check_gemm_act(M, N, K, w, y, bias, amax, yq, yq_scale)
     epi = _epilogue_act(M, N, bias, activation, residual, amax, yq, yq_scale, yq_fmt)
     _on_current_device(x, w, w_scale, y, workspace, bias, residual, amax, yq, yq_scale, dev_status)
     if hist is not None:
         _on_current_device(hist.ring, hist.pending, hist.ticket)
+    if K and N:
+        _check_scale("w_scale", w_scale, w_mode, N, K)
     rc = _lib.fp8_linear_forward_act(_ptr(x), M, K, ldx, x_fmt, x_mode,
                                      ctypes.byref(hist.c) if hist is not None else None, _ptr(w), _ptr(w_scale),
                                      w_mode, w_fmt, N, _ptr(y), ldy, ctypes.byref(epi), _ptr(dev_status),

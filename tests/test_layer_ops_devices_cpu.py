@@ -127,6 +127,55 @@ def test_each_tensor_is_guarded(op, place, calls):
     assert len(calls) == 1
 
 
+BAD_SHAPES = [dict(y=(4, 7)), dict(y=(3, 8)), dict(y=(8, 4)), dict(yq=(4, 9)), dict(yq=(2, 8)), dict(residual=(4, 7)),
+              dict(bias=(7,))]
+
+
+@pytest.mark.parametrize("op", ["gemm", "linear"])
+def test_shapes_of_the_activation_gemm(op, calls):
+    """What a kernel would read or write past the end of: outputs that are not [M, N], operands of another K, scale
+    buffers that are too short; and views whose elements are not where the call takes them to be."""
+    call, make = CALLS[op]
+    extra = dict(hist=history())
+    wt, ws = ("b", "b_scale") if op == "gemm" else ("w", "w_scale")
+    bad = [{n: here(*shape, dtype=make()[n].dtype)} for d in BAD_SHAPES for n, shape in d.items()]
+    bad += [{wt: here(8, 48, dtype=U8)}, {wt: here(8, 64, dtype=U8)[:, :32]}, {wt: here(256, dtype=U8)},
+            {ws: here(7, dtype=F32)}, {ws: here(8, dtype=U8)}, {ws: here(8, 2, dtype=F32)[:, 0]},
+            {"y": here(4, 16, dtype=BF)[:, ::2]}, {"yq": here(8, 4, dtype=U8).t()}, {"bias": here(16, dtype=BF)[::2]},
+            {"amax": here(0, dtype=F32)}, {"amax": here(1, dtype=BF)}, {"yq_scale": here(1, dtype=BF)}]
+    if op == "gemm":
+        bad += [dict(a=here(4, 64, dtype=U8)[:, :32]), dict(a=here(128, dtype=U8)), dict(a_scale=here(3, dtype=F32))]
+    else:
+        bad += [dict(x=here(4, 64, dtype=BF)[:, ::2]), dict(x=here(128, dtype=BF)), dict(x=here(32, 4, dtype=BF).t())]
+    for kw in bad:
+        with pytest.raises(TypeError):
+            call(make() | extra | kw)
+    assert not calls
+    good = [dict(y=None), dict(y=here(4, 24, dtype=BF)[:, 8:16]), dict(yq=here(4, 11, dtype=U8)[:, 3:]), dict(yq=None)]
+    for kw in good:
+        call(make() | extra | kw)
+    assert len(calls) == len(good)
+
+
+def test_scale_buffers_of_every_mode(calls):
+    M, N, K = 4, 130, 256
+    t = dict(y=here(M, N, dtype=BF), a=here(M, K, dtype=U8), b=here(N, K, dtype=U8))
+
+    def run(am, sa, bm, sb):
+        b.fp8_scaled_gemm_act(t["a"], sa, am, 0, t["b"], sb, bm, 0, t["y"], activation=1, stream=0)
+    B1, B128, MX = b.FP8_SCALE_BLOCK_1x128, b.FP8_SCALE_BLOCK_128x128, b.FP8_SCALE_MX32
+    run(B1, here(4, 2, dtype=F32), B128, here(2, 2, dtype=F32))
+    run(MX, here(4, 8, dtype=U8), MX, here(N, 8, dtype=U8).view(torch.float8_e8m0fnu))
+    run(0, here(1, dtype=F32), 5, here(1, dtype=F32))
+    assert len(calls) == 3
+    for args in ((B1, here(4, 2, dtype=F32), B128, here(1, 2, dtype=F32)), (B1, here(4, 1, dtype=F32), B128, here(2, 2, dtype=F32)),
+                 (MX, here(4, 8, dtype=U8), MX, here(N, 7, dtype=U8)), (MX, here(4, 8, dtype=F32), MX, here(N, 8, dtype=U8)),
+                 (0, here(0, dtype=F32), 1, here(N, dtype=F32))):
+        with pytest.raises(TypeError):
+            run(*args)
+    assert len(calls) == 3
+
+
 def test_a_cache_is_on_one_device():
     for i in range(4):
         t = [here(4, 2, 16, 64, dtype=U8), here(4, 2, 16, 64, dtype=U8), here(4, 2, dtype=F32), here(4, 2, dtype=F32)]
