@@ -243,7 +243,8 @@ __device__ __forceinline__ float sigmoid_times(float v, float z) {
 // v Phi(v) = max(v, 0) - |v| / 2 erfc(|v| / sqrt(2)).  With x = |v| / sqrt(2) and t = 1 / (1 + 0.425 x),
 // erfc(x) exp(x^2) is a polynomial of degree 6 in t without constant term (a form of Hastings,
 // "Approximations for Digital Computers", 1955; coefficients fitted here for the least largest
-// relative error over 0 <= x <= 9.5, 2^-17).  The CUDA function erfcf took most of the epilogue's
+// relative error over 0 <= x <= 9.5, 2^-17; the exponent, up to 125 in fp32, adds as much again at the
+// tail's far end).  The CUDA function erfcf took most of the epilogue's
 // time: 4096 x 28672 x 8192 with bias, GELU and residual 1040 us, with this form 720 us.
 __device__ __forceinline__ float gelu(float v) {
     const float a = fabsf(v);
@@ -253,7 +254,8 @@ __device__ __forceinline__ float gelu(float v) {
     q = fmaf(q, t, 0.288957417011261f);
     q = fmaf(q, t, 0.22776003181934357f);
     q = fmaf(q, t, 0.24058204889297485f);
-    const float tail = 0.5f * a * (q * t) * exp2f(-0.72134752f * a * a);   // exp(-v^2 / 2)
+    // exp(-v^2 / 2), which is 0 beyond |v| = 16; the clamp keeps an infinite |v| from making that 0 a NaN
+    const float tail = 0.5f * fminf(a, 16.0f) * (q * t) * exp2f(-0.72134752f * a * a);
     return fmaxf(v, 0.0f) - tail;
 }
 template <int ACT>

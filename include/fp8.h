@@ -354,6 +354,9 @@ FP8_API int32_t fp8_linear_forward_noalloc(const void* x_dev, int64_t M, int64_t
  * and then y, amax and yq as described with fp8_epilogue_t (whose options `base` holds).
  *   activation    GELU = v Phi(v) (erf form); GELU_TANH = its tanh approximation
  *                 0.5 v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))); SILU = v / (1 + exp(-v)).
+ *                 v = +inf (a product that overflowed, an infinite bias) gives +inf; v = -inf gives
+ *                 the limit 0 with RELU and GELU, NaN with the two others, whose formulas are
+ *                 -inf * 0 there.
  *   residual_dev  nullable bf16 [M, N], row stride ldres >= N, 2-byte aligned (fastest with
  *                 ldres % 8 == 0 and a 16-byte aligned base).  It may be y_dev itself
  *                 (same address and stride: y is then accumulated into); otherwise it must
