@@ -832,6 +832,7 @@ size_t attention_workspace(int32_t batch, int32_t q_heads, int32_t kv_heads, int
 cudaError_t launch_kv_attention(const AttnArgs& a, cudaStream_t st) {
     AttnParams p{};
     p.c = a.c;
+    p.c.max_q = (int32_t)std::min<int64_t>(a.c.max_q, a.c.tokens);     // a loose bound sizes nothing
     p.q = a.q;
     p.out = a.out;
     p.ldq = a.ldq;

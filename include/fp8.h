@@ -498,8 +498,8 @@ FP8_API int32_t fp8_kv_append(const fp8_kv_cache_t* cache, const void* k_dev, in
  * out is rounded once to bf16.  A query that sees no token (kv_len 0) gives zeros.
  *   q_dev, out_dev  bf16 [tokens][q_heads][head_dim], token strides ldq / ldo (% 8 == 0,
  *                   >= q_heads head_dim), 16-byte aligned.  q is finite; out does not overlap it.
- *   q_heads         a multiple of kv_heads.
- *   max_kv_len      bounds every kv_lens[b].  It and max_q_len size the launch.
+ *   q_heads         a multiple of kv_heads, <= 65536; min(max_q_len, tokens) q_heads <= 2^31 - 2^16.
+ *   max_kv_len      bounds every kv_lens[b], < 2^30.  It and max_q_len (< 2^24) size the launch.
  *   softmax_scale   finite.
  *   workspace       fp8_kv_attention_workspace_size bytes, 16-byte aligned, needs no
  *                   initialisation; calls that share one must not overlap on the GPU.
