@@ -152,13 +152,15 @@ __global__ void __launch_bounds__(WARP ? 32 * WARP_ROWS : 1024) rmsnorm_quantize
             if (k < p.nvec) st_v4_stream(p.sum + row * p.lds + k * NVEC, pack8(h[j]));
         }
     }
-    // 1 / sqrt(mean + eps); squares that leave the fp32 range (|h| above 1e19) are summed
-    // again at 2^-80 of their size.  The branch is the same for the whole row.
+    // 1 / sqrt(mean + eps).  Where that leaves the range in which fp32 holds it to 24 bits (|h| above
+    // 1e19; an eps near either end), the squares are summed again at 2^-80 (or 2^60) of h, and eps at
+    // its square.  The branch is the same for the whole row.
     float rstd;
-    if (ss <= 3.402823466e38f) {
-        rstd = __frsqrt_rn(fmaf(ss, p.inv_cols, p.eps));
+    const float mean = fmaf(ss, p.inv_cols, p.eps);
+    if (mean >= 7.888609052210118e-31f && mean <= 3.402823466e38f) {              // 2^-100
+        rstd = __frsqrt_rn(mean);
     } else {
-        const float pre = 8.271806125530277e-25f;     // 2^-80
+        const float pre = mean < 1.0f ? 1.152921504606847e18f : 8.271806125530277e-25f;    // 2^60, 2^-80
         float s2 = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
@@ -167,8 +169,8 @@ __global__ void __launch_bounds__(WARP ? 32 * WARP_ROWS : 1024) rmsnorm_quantize
                 s2 = fmaf(h[j][i].x * pre, h[j][i].x * pre, s2);
                 s2 = fmaf(h[j][i].y * pre, h[j][i].y * pre, s2);
             }
-        // eps is far below; the product may be subnormal, with 21 bits at least
-        rstd = pre * __frsqrt_rn(group_sum<WARP>(s2, red_sum[1]) * p.inv_cols);
+        // at 2^-80 the product may be subnormal, with 21 bits at least
+        rstd = pre * __frsqrt_rn(fmaf(group_sum<WARP>(s2, red_sum[1]), p.inv_cols, p.eps * pre * pre));
     }
     // h becomes -y
     float m[VPT];
