@@ -97,8 +97,9 @@ __device__ __forceinline__ float max_abs_nan(float a, float b) {
 }
 
 // MODE: fp8_scaling_t.  VPT: 16-byte vectors of a row per thread.  WARP: a warp per row
-// (rows of up to 32 VPT vectors), else the CTA (blockDim.x >= nvec / VPT).
-template <int FMT, int MODE, int VPT, bool WARP>
+// (rows of up to 32 VPT vectors), else the CTA (blockDim.x >= nvec / VPT).  ANY_EPS: for an eps that the plain
+// forms of the root do not serve (see launch_mode).
+template <int FMT, int MODE, int VPT, bool WARP, bool ANY_EPS>
 __global__ void __launch_bounds__(WARP ? 32 * WARP_ROWS : 1024) rmsnorm_quantize_kernel(const NormParams p) {
     __shared__ float red_sum[2][32];
     __shared__ uint32_t red_max[32];
@@ -152,15 +153,11 @@ __global__ void __launch_bounds__(WARP ? 32 * WARP_ROWS : 1024) rmsnorm_quantize
             if (k < p.nvec) st_v4_stream(p.sum + row * p.lds + k * NVEC, pack8(h[j]));
         }
     }
-    // 1 / sqrt(mean + eps).  Where that leaves the range in which fp32 holds it to 24 bits (|h| above
-    // 1e19; an eps near either end), the squares are summed again at 2^-80 (or 2^60) of h, and eps at
-    // its square.  The branch is the same for the whole row.
+    // 1 / sqrt(mean + eps); squares that leave the fp32 range (|h| above 1e19) are summed again at 2^-80 of
+    // their size, where eps is far below; with ANY_EPS also a sum that eps takes out of the range or
+    // leaves near subnormals, at 2^60 then, and eps at the square.  The branch is the same for the whole row.
     float rstd;
-    const float mean = fmaf(ss, p.inv_cols, p.eps);
-    if (mean >= 7.888609052210118e-31f && mean <= 3.402823466e38f) {              // 2^-100
-        rstd = __frsqrt_rn(mean);
-    } else {
-        const float pre = mean < 1.0f ? 1.152921504606847e18f : 8.271806125530277e-25f;    // 2^60, 2^-80
+    auto again = [&](float pre) {
         float s2 = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
@@ -169,8 +166,19 @@ __global__ void __launch_bounds__(WARP ? 32 * WARP_ROWS : 1024) rmsnorm_quantize
                 s2 = fmaf(h[j][i].x * pre, h[j][i].x * pre, s2);
                 s2 = fmaf(h[j][i].y * pre, h[j][i].y * pre, s2);
             }
+        s2 = group_sum<WARP>(s2, red_sum[1]) * p.inv_cols;
         // at 2^-80 the product may be subnormal, with 21 bits at least
-        rstd = pre * __frsqrt_rn(fmaf(group_sum<WARP>(s2, red_sum[1]), p.inv_cols, p.eps * pre * pre));
+        return pre * __frsqrt_rn(ANY_EPS ? fmaf(p.eps * pre, pre, s2) : s2);
+    };
+    const float down = 8.271806125530277e-25f, up = 1.152921504606847e18f;                     // 2^-80, 2^60
+    if (!ANY_EPS) {
+        if (ss <= 3.402823466e38f) rstd = __frsqrt_rn(fmaf(ss, p.inv_cols, p.eps));
+        else                       rstd = again(down);
+    } else {
+        const float mean = fmaf(ss, p.inv_cols, p.eps);
+        if (mean < 7.888609052210118e-31f)   rstd = again(up);                                  // 2^-100
+        else if (!(mean <= 3.402823466e38f)) rstd = again(down);
+        else                                 rstd = __frsqrt_rn(mean);
     }
     // h becomes -y
     float m[VPT];
@@ -256,17 +264,22 @@ __global__ void __launch_bounds__(WARP ? 32 * WARP_ROWS : 1024) rmsnorm_quantize
     }
 }
 
-template <int FMT, int MODE, int VPT, bool WARP>
+template <int FMT, int MODE, int VPT, bool WARP, bool ANY_EPS = false>
 cudaError_t launch_one(const NormParams& p, cudaStream_t st) {
     const int64_t grid = WARP ? (p.rows + WARP_ROWS - 1) / WARP_ROWS : p.rows;
     const int per = (p.nvec + VPT - 1) / VPT;
     const int threads = WARP ? 32 * WARP_ROWS : std::max(32, (per + 31) / 32 * 32);
-    rmsnorm_quantize_kernel<FMT, MODE, VPT, WARP><<<(unsigned)grid, threads, 0, st>>>(p);
+    rmsnorm_quantize_kernel<FMT, MODE, VPT, WARP, ANY_EPS><<<(unsigned)grid, threads, 0, st>>>(p);
     return cudaGetLastError();
 }
 
 template <int FMT, int MODE>
 cudaError_t launch_mode(const NormParams& p, cudaStream_t st) {
+    // Below 2^-126 eps does not cover the rounding of subnormal squares, and above 2^88 it counts beside sums that
+    // leave fp32 or takes them there.  These rows have an instance of their own: in the others its
+    // branches would cost registers, and with them 5 to 10 % (1021 x 5152, MX32: 5.8 and 6.3 us).
+    if (!(p.eps >= 1.1754943508e-38f && p.eps <= 3.0948500982e26f))
+        return p.nvec <= 128 ? launch_one<FMT, MODE, 4, true, true>(p, st) : launch_one<FMT, MODE, 4, false, true>(p, st);
     if (p.nvec <= 32) return launch_one<FMT, MODE, 1, true>(p, st);
     if (p.nvec <= 64) return launch_one<FMT, MODE, 2, true>(p, st);
     if (p.nvec <= 128) return launch_one<FMT, MODE, 4, true>(p, st);
