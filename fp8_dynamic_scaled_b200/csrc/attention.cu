@@ -259,6 +259,7 @@ __device__ __forceinline__ void produce(const AttnParams& p, const CUtensorMap& 
                 row[g] = (int32_t)(at * P + tok % P);
                 si.ks[g] = __ldg(p.c.k_scale + at);
                 const float vs = __ldg(p.c.v_scale + at);
+                if (!v_scale_ok(vs)) report_status(p.c.status, FP8_ERR_INVALID_ARG);
                 si.lv[g] = __log2f(vs) + P_SHIFT;
                 si.iv[g] = __frcp_rn(vs);
                 si.valid[g] = min(16, c.sees - tok);

@@ -32,6 +32,10 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// The range of the V scales, 2^-56 to 2^24 (reported otherwise).  A weight w is 0 below 2^-126, while w / s_v counts
+// in the softmax's sum whatever s_v is; and a part of the sum is dropped when its maximum is that far
+// below another's.  With scales at most 2^80 apart what is lost is 2^-39 of the sum per token.
+__device__ __forceinline__ bool v_scale_ok(float vs) { return vs >= 1.3877787807814457e-17f && vs <= 16777216.0f; }
 // Four codes -> two pairs of fp16 values, exactly.
 template <int FMT>
 __device__ __forceinline__ void half2x2_of(uint32_t codes, uint32_t& lo, uint32_t& hi) {

@@ -166,6 +166,7 @@ __device__ __forceinline__ void convert(const AttnParams& p, const Unit& u, uint
         }
         __syncwarp();
         fetch(batch + 1);
+        if (!v_scale_ok(vs)) report_status(p.c.status, FP8_ERR_INVALID_ARG);
     };
     Codes<FMT, D> k, v;
     fetch(0);

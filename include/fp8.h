@@ -431,7 +431,8 @@ FP8_API int32_t fp8_rmsnorm_quantize(const void* x_dev, int64_t rows, int64_t co
  *                    (E4M3 or E5M2), 16-byte aligned.
  *   k_scale_dev, v_scale_dev  float [num_pages][kv_heads]: one dequantisation multiplier per
  *                    page and KV head, positive and finite.  fp8_kv_append writes powers of
- *                    two.
+ *                    two, 2^-55 (a page of zeros, E5M2) to 2^120 (bf16's largest, E4M3).  Those of
+ *                    V that fp8_kv_attention reads are from 2^-56 to 2^24.
  *   page_size        16, 32, 64 or 128 tokens.   head_dim  64 or 128.
  *   page_table_dev   int32 [batch][table_stride]: entry i of row b is the page of the tokens
  *                    [i page_size, (i + 1) page_size) of sequence b; max_pages <= table_stride
@@ -448,7 +449,8 @@ FP8_API int32_t fp8_rmsnorm_quantize(const void* x_dev, int64_t rows, int64_t co
  * What only the device sees is checked there: a sequence with a bad cu_q, with more tokens
  * than max_q_len or than its page-table row or max_kv_len allows, or a page index outside
  * [0, num_pages) sets FP8_ERR_INVALID_ARG in dev_status; nothing is then read or written for
- * that sequence or page (fp8_kv_attention: those outputs are unspecified).
+ * that sequence or page (fp8_kv_attention: those outputs are unspecified, as those of a sequence with a
+ * V scale out of range, which sets FP8_ERR_INVALID_ARG too).
  */
 typedef struct {
     uint8_t* k_dev;
@@ -494,7 +496,9 @@ FP8_API int32_t fp8_kv_append(const fp8_kv_cache_t* cache, const void* k_dev, in
  * over the tokens j of the query's sequence up to and including its own position, k_j and v_j
  * the dequantised cache (decode(code) scale) of KV head h / (q_heads / kv_heads).  The codes
  * are decoded on chip (exactly); scores, softmax and sums are in fp32, the products' operands
- * in fp16 (codes exactly; a query row after a power-of-two normalisation; the weights p),
+ * in fp16 (codes exactly; a query row after a power-of-two normalisation; the weights p, each
+ * times its page's V scale: one below 2^-22 of its row's largest such product loses bits in the sum
+ * over v, below 2^-33 it is 0 there; the softmax's own sum is not affected),
  * out is rounded once to bf16.  A query that sees no token (kv_len 0) gives zeros.
  *   q_dev, out_dev  bf16 [tokens][q_heads][head_dim], token strides ldq / ldo (% 8 == 0,
  *                   >= q_heads head_dim), 16-byte aligned.  q is finite; out does not overlap it.
