@@ -249,13 +249,13 @@ __device__ __forceinline__ float sigmoid_times(float v, float z) {
 __device__ __forceinline__ float gelu(float v) {
     const float a = fabsf(v);
     const float t = __fdividef(1.0f, fmaf(0.30052038f, a, 1.0f));          // 0.425 / sqrt(2)
-    float q = fmaf(-0.1549525260925293f, t, 0.43133246898651123f);
-    q = fmaf(q, t, -0.03367231786251068f);
-    q = fmaf(q, t, 0.288957417011261f);
-    q = fmaf(q, t, 0.22776003181934357f);
-    q = fmaf(q, t, 0.24058204889297485f);
+    float q = fmaf(-0.07747626304626465f, t, 0.21566623449325562f);                          // half of the polynomial
+    q = fmaf(q, t, -0.01683615893125534f);
+    q = fmaf(q, t, 0.1444787085056305f);
+    q = fmaf(q, t, 0.11388001590967178f);
+    q = fmaf(q, t, 0.12029102444648743f);
     // exp(-v^2 / 2), which is 0 beyond |v| = 16; the clamp keeps an infinite |v| from making that 0 a NaN
-    const float tail = 0.5f * fminf(a, 16.0f) * (q * t) * exp2f(-0.72134752f * a * a);
+    const float tail = fminf(a, 16.0f) * (q * t) * exp2f(-0.72134752f * a * a);
     return fmaxf(v, 0.0f) - tail;
 }
 template <int ACT>
