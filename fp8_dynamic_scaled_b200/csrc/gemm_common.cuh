@@ -26,8 +26,9 @@ constexpr uint64_t DRAIN_LIMIT_NS = 2000000000ull;    // 2 s: limit of a wait fo
 
 
 // What a kernel instance's epilogue can do: plain bf16 output; bias / output amax / FP8
-// output; those and an activation and a residual.  Each is its own instance, so that
-// the options cost nothing where they are not asked for.
+// output; those and an activation, a residual and FP8 rows of any alignment.  Each is its own instance,
+// so that the options cost nothing where they are not asked for (the turning of unaligned FP8 rows
+// alone took 2 to 9 % of a short K's time: 2048 x 8192 x 1024 with bias and FP8 output 46.2 us without, 49.9 with).
 enum { EPI_PLAIN = 0, EPI_OPTIONS = 1, EPI_ACT = 2 };
 
 struct GemmParams {
@@ -156,21 +157,11 @@ __device__ __forceinline__ void stage_row_sw64(uint8_t* buf, int r, const uint32
 // stores; it commits an empty group, since the buffers' reuse counts one group per chunk.
 __device__ __forceinline__ void store_chunk(const CUtensorMap* tmY, uint8_t* buf, const uint32_t (&w)[16],
                                             int32_t x, int32_t y, int lane, const GemmParams& p, int32_t n_lim) {
-    const bool partial = (n_lim & 7) != 0 && n_lim - x < 32;
-    if (p.y_direct || partial) {
-        const int32_t row = y + lane;
-        if (p.y_vec && n_lim - x >= 32 && (x & 7) == 0) {
-            if (row < p.M) {
-                uint4* d4 = reinterpret_cast<uint4*>(p.y + (int64_t)row * p.ldy + x);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) d4[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-            }
-            return;
-        }
-        // rows of any alignment: through the staging buffer, then a row per store, a column per lane
+    stage_row_sw64(buf, lane, w);
+    if (p.y_direct || ((n_lim & 7) != 0 && n_lim - x < 32)) {
+        // rows of any alignment: from the staging buffer a row per store, a column per lane
         // (a lane that stores its own row touches 32 sectors at a time: 2048 x 8191 outputs, K = 1024
         // took 181 us, this way 60 us)
-        stage_row_sw64(buf, lane, w);
         __syncwarp();
         const int32_t rows = min(32, p.M - y);
         if (x + lane < n_lim) {
@@ -185,7 +176,6 @@ __device__ __forceinline__ void store_chunk(const CUtensorMap* tmY, uint8_t* buf
         if (lane == 0 && !p.y_direct) ptx::bulk_commit();
         return;
     }
-    stage_row_sw64(buf, lane, w);
     ptx::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
@@ -339,7 +329,7 @@ struct ResidualChunk {
 // f[] are the scaled fp32 accumulators, res the row's residual (EPI_ACT with one).  Adds the bias,
 // applies the activation and adds the residual, rounds to bf16 (w, for the Y store), folds |y| into the running
 // maximum and writes the FP8 output codes.  `buf`: 2 KB that the warp's 32 lanes (32 consecutive rows)
-// may use to turn codes whose rows are not 16-byte aligned, or null (each lane then writes its own).
+// may use to turn codes whose rows are not 16-byte aligned (EPI_ACT), or null (each lane then writes its own).
 template <int EXT>
 __device__ __forceinline__ void epi_chunk(const GemmParams& p, EpiState& es, float (&f)[32], const uint32_t (&res)[16],
                                           int32_t n0, int32_t n_lim, int32_t row, uint32_t (&w)[16],
@@ -380,7 +370,7 @@ __device__ __forceinline__ void epi_chunk(const GemmParams& p, EpiState& es, flo
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
-    const bool turn = p.yq && !p.yq_vec && buf != nullptr;       // the same for all lanes
+    const bool turn = EXT == EPI_ACT && p.yq && !p.yq_vec && buf != nullptr;       // the same for all lanes
     if (row >= p.M && !turn) return;
     if (p.amax && row < p.M) {
 #pragma unroll

@@ -349,7 +349,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     const int32_t n0 = nb * BN + c * 32;
                     uint32_t w[16];
                     uint8_t* b = ybuf + (store_it % C::STAGE_BUFS) * 2048;
-                    if (EXT && p.turns) {
+                    if (EXT == EPI_ACT && p.turns) {
                         if (lane == 0) ptx::bulk_wait_read<C::STAGE_BUFS - 1>();
                         __syncwarp();
                     }
@@ -435,7 +435,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     const int32_t n0 = nb * BN + half * 128 + c * 32;
                     uint32_t w[16];
                     uint8_t* b = ybuf + (store_it % C::STAGE_BUFS) * 2048;
-                    if (EXT && p.turns) {
+                    if (EXT == EPI_ACT && p.turns) {
                         if (lane == 0) ptx::bulk_wait_read<C::STAGE_BUFS - 1>();
                         __syncwarp();
                     }
@@ -480,7 +480,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     const int32_t n0 = nb * BN + half * 128 + c * 32;
                     uint32_t w[16];
                     uint8_t* b = ybuf + (store_it % C::STAGE_BUFS) * 2048;
-                    if (EXT && p.turns) {
+                    if (EXT == EPI_ACT && p.turns) {
                         if (lane == 0) ptx::bulk_wait_read<C::STAGE_BUFS - 1>();
                         __syncwarp();
                     }
@@ -718,7 +718,7 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 const int32_t n0 = nb * BN + c * 32;
                 uint32_t w[16];
                 uint8_t* b = ybuf + (store_it % S::STAGE_BUFS) * 2048;
-                if (EXT && p.turns) {
+                if (EXT == EPI_ACT && p.turns) {
                     if (lane == 0) ptx::bulk_wait_read<S::STAGE_BUFS - 1>();
                     __syncwarp();
                 }
@@ -882,7 +882,7 @@ static void set_epilogue(const GemmArgs& g, GemmParams& p) {
     p.ldq = g.ldq;
     p.yq_vec = (g.yq != nullptr && (reinterpret_cast<uintptr_t>(g.yq) & 15u) == 0 && g.ldq % 16 == 0) ? 1 : 0;
     p.ext = (g.bias != nullptr || g.amax != nullptr || g.yq != nullptr) ? EPI_OPTIONS : EPI_PLAIN;
-    if (g.activation != FP8_ACT_NONE || g.residual != nullptr) p.ext = EPI_ACT;
+    if (g.activation != FP8_ACT_NONE || g.residual != nullptr || (g.yq != nullptr && !p.yq_vec)) p.ext = EPI_ACT;
     p.activation = g.activation;
     p.res = g.residual;
     p.ldres = g.ldres;
