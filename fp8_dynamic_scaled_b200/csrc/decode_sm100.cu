@@ -143,13 +143,18 @@ fp8_decode_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                 if (w_part) {
                     ptx::mbar_arrive_expect_tx(&full[stage], (uint32_t)kbs * (uint32_t)(w + d.nt) * BK);
                     // row group by row group, each group's K blocks back to back
-                    for (int32_t r = 0; r < w;) {
-                        const int32_t box = w - r >= 64 ? 64 : w - r >= 32 ? 32 : D_UNIT;
-                        const CUtensorMap* tm = box == 64 ? &tmW64 : box == 32 ? &tmW32 : &tmW16;
+                    auto rows = [&](const CUtensorMap* tm, int32_t r) {
+#pragma unroll 1                                              // unrolled, 64 tokens lose 3 %
                         for (int32_t b = 0; b < kbs; ++b)
                             ptx::tma_load_2d(st + b * D_TILE_BYTES + r * BK, tm, &full[stage], (kb0 + b) * BK, n0 + r);
-                        r += box;
+                    };
+                    int32_t r = 0;
+                    for (; w - r >= 64; r += 64) rows(&tmW64, r);
+                    if (w - r >= 32) {
+                        rows(&tmW32, r);
+                        r += 32;
                     }
+                    if (r < w) rows(&tmW16, r);
                 }
                 if (x_part)
                     for (int32_t b = 0; b < kbs; ++b)
@@ -333,10 +338,12 @@ static cudaError_t launch_decode_t(const GemmArgs& g, GemmParams p, cudaStream_t
     // M = 128 weight rows, N = nt tokens
     p.idesc = (1u << 4) | ((uint32_t)g.fmt_b << 7) | ((uint32_t)g.fmt_a << 10) | ((uint32_t)(d.nt >> 3) << 17) |
               ((uint32_t)(D_TILE >> 4) << 24);
-    // equal shares: as many units for every CTA as the largest share has anyway (N = 8192, K = 28672:
-    // 128 CTAs of 64 rows 52 us, 148 CTAs of 48 or 64 rows 77 us)
+    // The largest share is `per` units either way.  Where it is even, equal shares on fewer CTAs: chunks of whole
+    // 32- and 64-row boxes (16 tokens, N = 8192, K = 8192: 128 CTAs of 64 rows 20.2 us, 148 of 48 or 64 rows 21.6).
+    // Where it is odd, all CTAs, most of which then have an even share (N = 10240: 128 CTAs of 80 rows 22.6 us, 148
+    // of 64 or 80 rows 22.2; N = 57344: 85.8 and 84.5).
     const int per = (d.units + num_sms() - 1) / num_sms();
-    const int grid = std::max(1, (d.units + per - 1) / per);
+    const int grid = std::max(1, per % 2 == 0 ? (d.units + per - 1) / per : std::min(d.units, num_sms()));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(D_THREADS);
