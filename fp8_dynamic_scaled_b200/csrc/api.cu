@@ -532,7 +532,8 @@ int32_t fp8_kv_attention(const fp8_kv_cache_t* cache, const void* q_dev, int64_t
     if (max_kv_len < 0 || max_kv_len >= ((int64_t)1 << 30) || max_q_len >= (1 << 24)) return FP8_ERR_INVALID_ARG;
     // rows (tokens x heads) are counted in int32, with room for the last tile
     if (std::min<int64_t>(max_q_len, tokens) * q_heads > ((int64_t)1 << 31) - (1 << 16)) return FP8_ERR_INVALID_ARG;
-    if (!(softmax_scale >= -3.402823466e38f && softmax_scale <= 3.402823466e38f)) return FP8_ERR_INVALID_ARG;
+    // the kernels work in units of log2: softmax_scale log2(e) is finite too (NaN fails as well)
+    if (!(softmax_scale >= -2.3586571e38f && softmax_scale <= 2.3586571e38f)) return FP8_ERR_INVALID_ARG;
     const bool none = tokens == 0 || cache->batch == 0 || max_q_len == 0;
     if (!none && (q_dev == nullptr || out_dev == nullptr)) return FP8_ERR_INVALID_ARG;
     if (ldq % 8 != 0 || ldo % 8 != 0 || !aligned16(q_dev) || !aligned16(out_dev)) return FP8_ERR_ALIGNMENT;

@@ -504,7 +504,9 @@ FP8_API int32_t fp8_kv_append(const fp8_kv_cache_t* cache, const void* k_dev, in
  *                   >= q_heads head_dim), 16-byte aligned.  q is finite; out does not overlap it.
  *   q_heads         a multiple of kv_heads, <= 65536; min(max_q_len, tokens) q_heads <= 2^31 - 2^16.
  *   max_kv_len      bounds every kv_lens[b], < 2^30.  It and max_q_len (< 2^24) size the launch.
- *   softmax_scale   finite.
+ *   softmax_scale   finite, |softmax_scale| <= 2.3586571e38 (its product with log2(e) is finite too).
+ *                   |softmax_scale| log2(e) times a query row's largest element, and every score,
+ *                   must be in the range of fp32; outputs of other rows are unspecified.
  *   workspace       fp8_kv_attention_workspace_size bytes, 16-byte aligned, needs no
  *                   initialisation; calls that share one must not overlap on the GPU.
  * The result does not depend on the batch's other sequences' contents (their lengths decide where

@@ -18,3 +18,10 @@ def test_rows_that_int32_cannot_count(kv_heads):
     assert sized((1 << 15) - 1, 1 << 16, kv_heads, (1 << 24) - 1) == b.FP8_ERR_WORKSPACE      # the most; a loose bound
     assert sized((1 << 31) - 1, 1 << 16, kv_heads, 16) == b.FP8_ERR_WORKSPACE
     assert sized((1 << 31) - 1, 1 << 16, kv_heads, 1 << 15) == INV
+
+
+def test_softmax_scale_times_log2e_is_finite():
+    for scale in (2.359e38, 3.4e38, float("nan")):
+        assert attend(scale=scale, ws=None) == INV and attend(scale=-scale, ws=None) == INV
+    for scale in (2.3586e38, -2.3586e38, 2.0 ** 90, 0.0):
+        assert attend(scale=scale, ws=None) == b.FP8_ERR_WORKSPACE
