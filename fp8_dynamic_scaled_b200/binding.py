@@ -539,6 +539,8 @@ def fp8_kv_attention(q, cache: KVCache, page_table, kv_lens, out, *, max_kv_len,
     softmax_scale defaults to head_dim ** -0.5."""
     if q.dim() != 3 or out.shape != q.shape:
         raise TypeError("q and out must be bf16 [tokens, q_heads, head_dim]")
+    if out.data_ptr() == q.data_ptr() and q.numel():
+        raise ValueError("out must not be q: heads of a row are written while others are still read")
     tokens, heads, dim = q.shape
     ldq = _head_rows(q, "q", heads, cache.head_dim)
     ldo = _head_rows(out, "out", heads, cache.head_dim)

@@ -176,6 +176,18 @@ def test_scale_buffers_of_every_mode(calls):
     assert len(calls) == 3
 
 
+def test_attention_into_its_own_queries_is_refused(calls):
+    call, make = CALLS["attend"]
+    t = make() | dict(cache=cache())
+    with pytest.raises(ValueError):
+        call(t | dict(out=t["q"]))
+    with pytest.raises(ValueError):
+        call(t | dict(out=t["q"].view(3, 4, 64)))
+    none = here(0, 4, 64, dtype=BF)
+    call(t | dict(q=none, out=none))
+    assert len(calls) == 1
+
+
 def test_a_cache_is_on_one_device():
     for i in range(4):
         t = [here(4, 2, 16, 64, dtype=U8), here(4, 2, 16, 64, dtype=U8), here(4, 2, dtype=F32), here(4, 2, dtype=F32)]
