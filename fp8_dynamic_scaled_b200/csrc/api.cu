@@ -517,7 +517,7 @@ size_t fp8_kv_attention_workspace_size(int32_t batch, int32_t q_heads, int32_t k
     if (batch <= 0 || kv_heads <= 0 || q_heads <= 0 || q_heads % kv_heads != 0 || max_q_len <= 0 || max_kv_len < 0 ||
         (head_dim != 64 && head_dim != 128))
         return 0;
-    return attention_workspace(batch, q_heads, kv_heads, head_dim, max_q_len, max_kv_len);
+    return attention_workspace(head_dim);
 }
 
 int32_t fp8_kv_attention(const fp8_kv_cache_t* cache, const void* q_dev, int64_t ldq, int32_t q_heads, int64_t tokens,

@@ -792,11 +792,14 @@ cudaError_t launch_attention(AttnParams p, cudaStream_t st) {
 }
 
 // Whether the prompt kernel's tiles of 128 rows serve a call better than this file's of 16, by what
-// both take (measured, D = 128): here 0.27 us per SM and work tile of 16 rows x 32 tokens, over all
+// both take (measured at D = 128 with sequences of one length, and used for D = 64 and ragged calls too): here 0.27 us per SM and work tile of 16 rows x 32 tokens, over all
 // SMs, after 14 us; there 2.1 us per step of 128 tokens after 7 us, one CTA per SM, whose SMs
 // are not shared among splits of a sequence.  E.g. 8 KV heads, 8 heads each, 4,096 cached
 // tokens: 64 new tokens of 1 sequence 85 us here and 92 there, 128 new tokens 147 and 92; of 8
-// sequences 4 new tokens 51 and 76, 16 new tokens 141 and 79.
+// sequences 4 new tokens 51 and 76, 16 new tokens 141 and 79.  It is off by up to 1.3 near its border (64 sequences
+// of 512 tokens, 4 new ones: 85 us chosen, 65 possible), and it is one choice for the whole call, by the bounds of
+// its longest sequence: 63 single tokens beside one chunk of 2048, all of 4,096 cached tokens, take 843 us, apart
+// 98 and 274.
 bool wide_tiles(const AttnParams& p) {
     const int64_t rows = (int64_t)p.c.max_q * p.group, units = (int64_t)p.c.batch * p.c.kv_heads;
     const double sms = num_sms();
@@ -813,21 +816,11 @@ cudaError_t launch_rows(const AttnParams& p, cudaStream_t st) {
     return launch_attention<FMT, D, 2>(p, st);
 }
 
-// The workspace: [2 grid][16][D] floats, the joins, then [2 grid][16] pairs.
-size_t workspace_bytes(int32_t head_dim) {
-    return (size_t)num_sms() * (2 * 16 * (size_t)(head_dim + 2) * sizeof(float) + sizeof(int4));
-}
-
 }  // namespace
 
-size_t attention_workspace(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t max_q,
-                           int64_t max_kv) {
-    (void)batch;
-    (void)q_heads;
-    (void)kv_heads;
-    (void)max_q;
-    (void)max_kv;
-    return workspace_bytes(head_dim);
+// The workspace: [2 grid][16][D] floats, the joins, then [2 grid][16] pairs.
+size_t attention_workspace(int32_t head_dim) {
+    return (size_t)num_sms() * (2 * 16 * (size_t)(head_dim + 2) * sizeof(float) + sizeof(int4));
 }
 
 cudaError_t launch_kv_attention(const AttnArgs& a, cudaStream_t st) {

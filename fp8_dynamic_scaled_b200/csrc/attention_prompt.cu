@@ -456,7 +456,8 @@ __global__ void __launch_bounds__(T_THREADS, 1) kv_prompt_attention_kernel(const
     uint8_t* k16 = q16 + 2 * tile_bytes<D>();
     uint8_t* v16 = k16 + 2 * tile_bytes<D>();
     const int warp = threadIdx.x >> 5;
-    // the CTAs with the most tokens to see (the last rows) come first
+    // of each sequence the CTAs with the most tokens to see (the last rows) come first; the sequences go side by side
+    // whatever their lengths
     const int32_t bh = p.c.batch * p.c.kv_heads;
     const int32_t rt = p.row_tiles - 1 - (int32_t)(blockIdx.x / bh);
     Unit u;

@@ -538,8 +538,9 @@ template <int EXT>
 struct PairSmem {
     // with an activation or a residual the epilogue outlasts the products of a short K: two warps
     // share each lane quarter then, half of the columns each (2048 x 8192 outputs, K = 1024: SiLU
-    // 55 -> 44 us, bias, GELU and residual 78 -> 59; 4096 x 28672, K = 8192, SiLU and FP8 output, where
-    // the products hide it: 713 -> 719)
+    // 48 -> 35 us, bias, GELU and residual 110 -> 78; 4096 x 28672, K = 8192, SiLU, where the products hide
+    // it: 811 both ways).  The instance without them still has four warps: a bias alone takes 38 us at the first
+    // size, a ReLU in this one 27.
     static constexpr int EPI_WARPS = EXT == EPI_ACT ? 8 : 4;
     static constexpr int FIRST_EPI_WARP = 3, STAGE_BUFS = 2;
     static constexpr int NT = (FIRST_EPI_WARP + EPI_WARPS) * 32;

@@ -146,9 +146,7 @@ struct AttnArgs {
     int64_t ldo;
     void* workspace;
 };
-// How a call's work is split: row tiles per (sequence, KV head) and splits of the cached tokens.
-size_t attention_workspace(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t max_q,
-                           int64_t max_kv);
+size_t attention_workspace(int32_t head_dim);
 cudaError_t launch_kv_attention(const AttnArgs& a, cudaStream_t st);
 
 }  // namespace fp8b

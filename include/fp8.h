@@ -446,7 +446,8 @@ FP8_API int32_t fp8_rmsnorm_quantize(const void* x_dev, int64_t rows, int64_t co
  * up.  cu_q_dev is int32 [batch + 1], non-decreasing; NULL means one token per sequence
  * (row b).  max_q_len bounds the tokens of one sequence.  Rows at or past cu_q[batch] are
  * neither read nor written.
- * What only the device sees is checked there: a sequence with a bad cu_q, with more tokens
+ * What only the device sees is checked there: a sequence with a bad cu_q, with more new tokens than
+ * kv_lens (fp8_kv_append; the attention gives zeros for those that see no token), with more tokens
  * than max_q_len or than its page-table row or max_kv_len allows, or a page index outside
  * [0, num_pages) sets FP8_ERR_INVALID_ARG in dev_status; nothing is then read or written for
  * that sequence or page (fp8_kv_attention: those outputs are unspecified, as those of a sequence with a
