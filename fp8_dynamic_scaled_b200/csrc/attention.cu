@@ -791,15 +791,15 @@ cudaError_t launch_attention(AttnParams p, cudaStream_t st) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Whether the prompt kernel's tiles of 128 rows serve a call better than this file's of 16, by what
-// both take (measured at D = 128 with sequences of one length, and used for D = 64 and ragged calls too): here 0.27 us per SM and work tile of 16 rows x 32 tokens, over all
-// SMs, after 14 us; there 2.1 us per step of 128 tokens after 7 us, one CTA per SM, whose SMs
-// are not shared among splits of a sequence.  E.g. 8 KV heads, 8 heads each, 4,096 cached
-// tokens: 64 new tokens of 1 sequence 85 us here and 92 there, 128 new tokens 147 and 92; of 8
-// sequences 4 new tokens 51 and 76, 16 new tokens 141 and 79.  It is off by up to 1.3 near its border (64 sequences
-// of 512 tokens, 4 new ones: 85 us chosen, 65 possible), and it is one choice for the whole call, by the bounds of
-// its longest sequence: 63 single tokens beside one chunk of 2048, all of 4,096 cached tokens, take 843 us, apart
-// 98 and 274.
+// Whether the prompt kernel's tiles of 128 rows serve a call better than this file's of 16, by what both
+// take (measured at D = 128 with sequences of one length, and used for D = 64 and ragged calls too): here 0.27 us
+// per SM and work tile of 16 rows x 32 tokens, over all SMs, after 14 us; there 2.1 us per step of 128 tokens
+// after 7 us, one CTA per SM, whose SMs are not shared among splits of a sequence.  E.g. 8 KV heads, 8 heads
+// each, 4,096 cached tokens: 64 new tokens of 1 sequence 85 us here and 92 there, 128 new tokens 147 and 92; of
+// 8 sequences 4 new tokens 51 and 76, 16 new tokens 141 and 79.  It is off by up to 1.3 near its border (64
+// sequences of 512 tokens, 4 new ones: 85 us chosen, 65 possible), and it is one choice for the whole call, by
+// the bounds of its longest sequence: 63 single tokens beside one chunk of 2048, all of 4,096 cached tokens,
+// take 843 us, apart 98 and 274.
 bool wide_tiles(const AttnParams& p) {
     const int64_t rows = (int64_t)p.c.max_q * p.group, units = (int64_t)p.c.batch * p.c.kv_heads;
     const double sms = num_sms();

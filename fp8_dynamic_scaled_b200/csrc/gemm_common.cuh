@@ -234,13 +234,13 @@ __device__ __forceinline__ float sigmoid_times(float v, float z) {
 // erfc(x) exp(x^2) is a polynomial of degree 6 in t without constant term (a form of Hastings,
 // "Approximations for Digital Computers", 1955; coefficients fitted here for the least largest
 // relative error over 0 <= x <= 9.5, 2^-17; the exponent, up to 125 in fp32, adds as much again at the
-// tail's far end).  With the CUDA function
-// erfcf the epilogue took longer than the products of a short K: 2048 x 8192 x 1024 with GELU 79 us, with this form
-// 41; 4096 x 28672 x 8192 with bias, GELU and residual, under the power cap, 956 and 845.
+// tail's far end).  With the CUDA function erfcf the epilogue took longer than the products of a short K:
+// 2048 x 8192 x 1024 with GELU 79 us, with this form 41; 4096 x 28672 x 8192 with bias, GELU and residual,
+// under the power cap, 956 and 845.
 __device__ __forceinline__ float gelu(float v) {
     const float a = fabsf(v);
     const float t = __fdividef(1.0f, fmaf(0.30052038f, a, 1.0f));          // 0.425 / sqrt(2)
-    float q = fmaf(-0.07747626304626465f, t, 0.21566623449325562f);                          // half of the polynomial
+    float q = fmaf(-0.07747626304626465f, t, 0.21566623449325562f);     // half of the polynomial
     q = fmaf(q, t, -0.01683615893125534f);
     q = fmaf(q, t, 0.1444787085056305f);
     q = fmaf(q, t, 0.11388001590967178f);
